@@ -77,9 +77,11 @@ enum {
     DLLM_ERR_WORKSPACE = -7,   /* workspace smaller than dllm_qgemm_workspace_bytes() asks     */
     DLLM_ERR_SCRATCH_LIMIT = -8, /* dllm_qgemm_noalloc: the call needs more scratch than the
                                     library's fixed array holds                              */
-    DLLM_ERR_SCALE_RANGE = -9   /* device-detected: dllm_repack_q5k met a block scale d with
+    DLLM_ERR_SCALE_RANGE = -9,  /* device-detected: dllm_repack_q5k met a block scale d with
                                    |d| >= 4096, which the split form cannot hold (16 d is not a
                                    finite f16); those blocks' fifth-bit part is not usable      */
+    DLLM_ERR_LOGITS = -10       /* device-detected: dllm_sample met a row of logits with a NaN or
+                                   +inf, or with no finite value; its token is -1               */
 };
 
 /* ------------------------------------------------------------------------------
@@ -302,8 +304,118 @@ int dllm_qkv_qgemm(const void* wq, const void* wk, const void* wv, dllm_qtype t,
 int dllm_attention(const void* q, const void* k, const void* v, int64_t Lq, int64_t Lk, int64_t H, int64_t Hkv,
                    int64_t dh, float* o, dllm_stream_t stream);
 
+/* ------------------------------------------------------------------------------
+ * Rotary positions (Architecture page, "A forward pass", step 2: RoPE between the Q/K/V
+ * projections and attention; "Source map", kernels/ops.mojo: its NORM and NEOX variants),
+ * with an optional RMSNorm of every query and key head in the same pass and the rounding
+ * of q, k and v to the f16 that dllm_attention and dllm_attention_masked read.
+ *
+ *   x = x * gamma / sqrt(mean(x^2) + eps)                       (heads with a gamma only)
+ *   (x1, x2) -> mscale * (x1 cos a - x2 sin a, x2 cos a + x1 sin a),
+ *   a = 2 pi * pos[t] * turns[i], for the pairs i in [0, n_rot / 2) of each head:
+ *   elements (2i, 2i + 1) in the NORM layout, (i, i + n_rot / 2) in the NEOX layout.
+ *   Elements from n_rot on pass through; v is only rounded.
+ *
+ * dllm_rope_turns (host only) fills the table of turns per position, turns[i] =
+ * f_i / (2 pi), and the factor mscale:
+ *   PLAIN   f_i = base^(-2 i / n_rot)
+ *   LINEAR  f_i / factor
+ *   NTK     base * factor^(n_rot / (n_rot - 2)) in place of base
+ *   YARN    f_i / factor * r_i + f_i * (1 - r_i), r_i = clamp((i - lo) / (hi - lo), 0, 1),
+ *           lo = max(floor(d(beta_fast)), 0), hi = min(ceil(d(beta_slow)), n_rot - 1),
+ *           d(b) = n_rot / 2 * ln(trained_len / (2 pi b)) / ln(base);
+ *           mscale = 0.1 ln(factor) + 1 for factor > 1 (else 1)
+ *   factor is read for every kind but PLAIN, trained_len and the betas for YARN only.
+ *   turns: host, n_rot / 2 doubles; the caller copies it to the device once per model.
+ *   Errors: DLLM_ERR_ARG (n_rot odd or < 0, base <= 1, factor <= 0, NTK with n_rot = 2,
+ *   YARN without 0 < beta_slow < beta_fast and trained_len > 0, null).
+ *
+ * dllm_qk_rope: q f32 [L][ldq] (H heads of dh), k and v f32 [L][ldk], [L][ldv] (Hkv heads),
+ *   as the projections write them: ld >= heads * dh, ld % 4 == 0; they may be column ranges
+ *   of one buffer.  v == NULL leaves v out.  dh % 8 == 0, dh <= 256; n_rot % 8 == 0,
+ *   n_rot <= dh (0: no rotation).  pos: device int32 [L], any value; NULL means 0 .. L - 1.
+ *   turns: device.  gamma_q, gamma_k: device f32 [dh], each may be NULL; with one given,
+ *   eps > 0.  oq f16 [L][H][dh], ok and ov f16 [L][Hkv][dh], contiguous, may not overlap
+ *   the inputs.  L == 0 is a no-op.
+ *   Arithmetic: the angle's turns in f64, reduced by the nearest whole number (every int32
+ *   position keeps an angle good to 2^-24 of a turn); norm sum and rotation in f32; one
+ *   rounding to f16 (|x| above 65504 becomes an infinity).
+ * Errors: DLLM_ERR_ARG, DLLM_ERR_ALIGN, DLLM_ERR_UNSUPPORTED, DLLM_ERR_CUDA.
+ * ---------------------------------------------------------------------------- */
+typedef enum { DLLM_ROPE_NORM = 0, DLLM_ROPE_NEOX = 2 } dllm_rope_layout;
+typedef enum { DLLM_ROPE_PLAIN = 0, DLLM_ROPE_LINEAR = 1, DLLM_ROPE_NTK = 2, DLLM_ROPE_YARN = 3 } dllm_rope_scaling;
+int dllm_rope_turns(int64_t n_rot, double base, dllm_rope_scaling kind, double factor, double trained_len,
+                    double beta_fast, double beta_slow, double* turns, float* mscale);
+int dllm_qk_rope(const float* q, int64_t ldq, const float* k, int64_t ldk, const float* v, int64_t ldv, int64_t L,
+                 int64_t H, int64_t Hkv, int64_t dh, const int32_t* pos, const double* turns, int64_t n_rot,
+                 dllm_rope_layout layout, float mscale, const float* gamma_q, const float* gamma_k, float eps,
+                 void* oq, void* ok, void* ov, dllm_stream_t stream);
+
+/* ------------------------------------------------------------------------------
+ * Attention under key intervals: query i attends to the keys [kv_begin[i], kv_end[i])
+ * only, with an optional cap on the scores and an optional bias by distance.
+ *
+ *   s_ij = cap * tanh(x_ij / cap), x_ij = q_i . k_j / sqrt(dh)      (cap = 0: s_ij = x_ij)
+ *   s_ij = s_ij - slopes[h] * |q_pos[i] - j|                        (slopes given)
+ *   o_i  = sum over the interval of softmax(s_i)_j v_j;  an empty interval gives zeros
+ *
+ * The interval covers, for a query at key position p:
+ *   packed documents    the bounds of the document that p lies in
+ *   prefix, causal      [0, max(prefix, p + 1))
+ *   blocks of B         [0, (p / B + 1) * B): a block denoised over the blocks before it
+ *   window              [p - w, p + w + 1)
+ *   padding             [0, 0)
+ * q: f16 [Lq][ldq] with H heads of dh; k, v: f16 [Lk][ldk], [Lk][ldv] with Hkv heads; head h
+ * reads key head h / (H / Hkv); ld >= heads * dh, ld % 8 == 0, so k and v may lie in a
+ * longer cache or in one fused buffer.  kv_begin, kv_end: device int32 [Lq]; NULL means 0,
+ * Lk; values are clamped to [0, Lk].  q_pos: device int32 [Lq], the queries' key positions
+ * (read with slopes only); NULL means i + Lk - Lq.  softcap >= 0, finite; slopes: device f32 [H] or
+ * NULL.  o: [Lq][H][dh] contiguous, f32 (what dllm_quantize_act reads) or f16 by o_type, may not
+ * overlap the inputs.  dh must be 128.  Lq == 0 is a no-op; Lk == 0 writes zeros.
+ * What keys hold outside a query's interval (NaN, infinities, memory never written) does
+ * not reach its output; a query that attends to a v with a NaN or an infinity is not finite.
+ * Precision as dllm_attention: f32 scores and softmax, weights rounded to f16 for P V.
+ * workspace: device scratch owned by the caller, at least
+ * dllm_attention_masked_workspace_bytes() bytes (may be 0, and at most 64 MiB); nothing in
+ * it carries over between calls, so calls ordered on one stream may share it.
+ * Errors: DLLM_ERR_ARG, DLLM_ERR_ALIGN, DLLM_ERR_WORKSPACE, DLLM_ERR_UNSUPPORTED,
+ * DLLM_ERR_CUDA; DLLM_ERR_TIMEOUT in the device error word.
+ * ---------------------------------------------------------------------------- */
+typedef enum { DLLM_F32 = 0, DLLM_F16 = 1 } dllm_ftype;
+int dllm_attention_masked_workspace_bytes(int64_t Lq, int64_t Lk, int64_t H, int64_t Hkv, size_t* bytes);
+int dllm_attention_masked(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                          int64_t Lq, int64_t Lk, int64_t H, int64_t Hkv, int64_t dh, const int32_t* kv_begin,
+                          const int32_t* kv_end, const int32_t* q_pos, float softcap, const float* slopes, void* o,
+                          dllm_ftype o_type, void* workspace, size_t workspace_bytes, dllm_stream_t stream);
+
+/* ------------------------------------------------------------------------------
+ * Sampling: one token per row of logits (what dllm_qgemm writes for the requested rows;
+ * Architecture page, "A forward pass", step 4; "Source map", diffusion/sampler.mojo), with
+ * the confidence and the entropy that order a denoising step's commits.
+ *
+ *   w_i = exp((l_i - max l) / temperature);  candidates by (l descending, index ascending)
+ *   kept: the first top_k candidates; of these the ones with w_i >= min_p; of these, of mass
+ *   S, the ones whose preceding mass is < top_p * S; and always the first candidate
+ *   token   = the first kept index, in index order, whose running mass exceeds u * kept mass
+ *   conf    = softmax(l)[token];  entropy = -sum p ln p of softmax(l)   (no limits, T = 1)
+ *
+ * logits: f32 [R][ldl], ldl >= V; -inf rules a word out.  Per row, device, each may be NULL:
+ * temperature (NULL: 1; <= 0 or NaN: greedy, the first candidate), top_k (NULL or <= 0: off),
+ * top_p (NULL or >= 1: off; <= 0 or NaN: the first candidate), min_p (NULL, <= 0 or NaN: off;
+ * above 1 counts as 1), u (NULL or NaN: 0; clamped to [0, 1], 1 gives the last kept).
+ * token: int32 [R]; conf, entropy: f32 [R], each may be NULL.  A row with a NaN or +inf, or
+ * without a finite logit, gets token -1, conf 0, entropy 0 and sets DLLM_ERR_LOGITS in the
+ * device error word.  R == 0 is a no-op.
+ * Weights and masses are 64-bit fixed point from an f64 exponential: the token is the same
+ * whatever the grid, and the same on every run.
+ * Errors: DLLM_ERR_ARG, DLLM_ERR_ALIGN, DLLM_ERR_UNSUPPORTED, DLLM_ERR_CUDA.
+ * ---------------------------------------------------------------------------- */
+int dllm_sample(const float* logits, int64_t R, int64_t V, int64_t ldl, const float* temperature, const int32_t* top_k,
+                const float* top_p, const float* min_p, const float* u, int32_t* token, float* conf, float* entropy,
+                dllm_stream_t stream);
+
 /* Synchronizes `stream`, then returns and clears the device error word
- * (DLLM_OK, DLLM_ERR_ROW_RANGE or DLLM_ERR_TIMEOUT). */
+ * (DLLM_OK, DLLM_ERR_ROW_RANGE, DLLM_ERR_TIMEOUT, DLLM_ERR_SCALE_RANGE or DLLM_ERR_LOGITS). */
 int dllm_get_device_status(dllm_stream_t stream);
 const char* dllm_status_string(int code);
 

@@ -783,6 +783,7 @@ const char* dllm_status_string(int code) {
         case DLLM_ERR_WORKSPACE: return "workspace too small";
         case DLLM_ERR_SCRATCH_LIMIT: return "call needs more scratch than the fixed no-allocation array holds";
         case DLLM_ERR_SCALE_RANGE: return "a Q5_K block scale d with |d| >= 4096: 16 d is not a finite f16";
+        case DLLM_ERR_LOGITS: return "a row of logits with a NaN or +inf, or without a finite value";
         default: return "unknown status";
     }
 }
@@ -987,3 +988,5 @@ int dllm_bench_mma_i8(int n, int n_acc, int a_from_tmem, int issuers, int iters,
 }
 
 }  // extern "C"
+
+#include "stepops.cuh"

@@ -1,0 +1,206 @@
+// Entry points of the operators between the projections of a step: dllm_rope_turns,
+// dllm_qk_rope, dllm_attention_masked and dllm_sample.  Part of dllm.cu (it uses its launch
+// and device helpers).
+#pragma once
+#include <cmath>
+
+#include "attmask.cuh"
+#include "rope.cuh"
+#include "sample.cuh"
+
+namespace {
+
+template <int G>
+cudaError_t launch_rope(const RopeArgs& a, dim3 grid, bool neox, cudaStream_t s) {
+    return neox ? launch_pdl(qk_rope_kernel<G, true>, grid, dim3(ROPE_THREADS), 0, s, a)
+                : launch_pdl(qk_rope_kernel<G, false>, grid, dim3(ROPE_THREADS), 0, s, a);
+}
+
+bool g_sample_attr_done[MAX_DEV];
+
+int status_of(cudaError_t e) {
+    if (e != cudaSuccess) {
+        (void)cudaGetLastError();
+        return DLLM_ERR_CUDA;
+    }
+    return launch_status();
+}
+
+}  // namespace
+
+extern "C" {
+
+int dllm_rope_turns(int64_t n_rot, double base, dllm_rope_scaling kind, double factor, double trained_len,
+                    double beta_fast, double beta_slow, double* turns, float* mscale) {
+    if (n_rot < 0 || n_rot % 2 || n_rot > 65536 || !(base > 1.0) || !(base < INFINITY) || !mscale) return DLLM_ERR_ARG;
+    if (n_rot > 0 && !turns) return DLLM_ERR_ARG;
+    if (kind != DLLM_ROPE_PLAIN && (!(factor > 0.0) || !(factor < INFINITY))) return DLLM_ERR_ARG;
+    const double two_pi = 6.283185307179586476925;
+    double lo = 0.0, span = 1.0;
+    *mscale = 1.0f;
+    switch (kind) {
+        case DLLM_ROPE_PLAIN:
+        case DLLM_ROPE_LINEAR: break;
+        case DLLM_ROPE_NTK:
+            if (n_rot == 2) return DLLM_ERR_ARG;  // n / (n - 2)
+            if (n_rot > 2) base *= std::pow(factor, (double)n_rot / (double)(n_rot - 2));
+            if (!(base > 0.0) || !(base < INFINITY)) return DLLM_ERR_ARG;
+            break;
+        case DLLM_ROPE_YARN: {
+            if (!(trained_len > 0.0) || !(trained_len < INFINITY) || !(beta_slow > 0.0) || !(beta_fast > beta_slow) ||
+                !(beta_fast < INFINITY))
+                return DLLM_ERR_ARG;
+            auto dim = [&](double beta) { return 0.5 * n_rot * std::log(trained_len / (beta * two_pi)) / std::log(base); };
+            lo = std::fmax(std::floor(dim(beta_fast)), 0.0);
+            const double hi = std::fmin(std::ceil(dim(beta_slow)), (double)n_rot - 1.0);
+            span = std::fmax(hi - lo, 0.001);
+            if (factor > 1.0) *mscale = (float)(0.1 * std::log(factor) + 1.0);
+            break;
+        }
+        default: return DLLM_ERR_ARG;
+    }
+    for (int64_t i = 0; i < n_rot / 2; i++) {
+        double f = std::pow(base, -2.0 * (double)i / (double)n_rot);
+        if (kind == DLLM_ROPE_LINEAR) f /= factor;
+        if (kind == DLLM_ROPE_YARN) {
+            const double ramp = std::fmin(std::fmax(((double)i - lo) / span, 0.0), 1.0);
+            f = f / factor * ramp + f * (1.0 - ramp);
+        }
+        turns[i] = f / two_pi;
+    }
+    return DLLM_OK;
+}
+
+int dllm_qk_rope(const float* q, int64_t ldq, const float* k, int64_t ldk, const float* v, int64_t ldv, int64_t L,
+                 int64_t H, int64_t Hkv, int64_t dh, const int32_t* pos, const double* turns, int64_t n_rot,
+                 dllm_rope_layout layout, float mscale, const float* gamma_q, const float* gamma_k, float eps,
+                 void* oq, void* ok, void* ov, dllm_stream_t stream) {
+    if (L < 0 || H <= 0 || Hkv <= 0 || dh <= 0 || dh > 256 || dh % 8 || n_rot < 0 || n_rot > dh || n_rot % 8)
+        return DLLM_ERR_ARG;
+    if (layout != DLLM_ROPE_NORM && layout != DLLM_ROPE_NEOX) return DLLM_ERR_ARG;
+    if (H > (1 << 20) || Hkv > (1 << 20) || L > (1LL << 31) - 1) return DLLM_ERR_ARG;
+    if (ldq < H * dh || ldk < Hkv * dh || (v && ldv < Hkv * dh)) return DLLM_ERR_ARG;
+    if (!(std::fabs(mscale) < INFINITY)) return DLLM_ERR_ARG;
+    if ((gamma_q || gamma_k) && (!(eps > 0.0f) || !(eps < INFINITY))) return DLLM_ERR_ARG;
+    if (L == 0) return DLLM_OK;
+    if (!q || !k || !oq || !ok || (v && !ov) || (n_rot > 0 && !turns)) return DLLM_ERR_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(oq) || !aligned16(ok) || (v && !aligned16(ov)) ||
+        !aligned16(pos) || !aligned16(turns) || !aligned16(gamma_q) || !aligned16(gamma_k) || ldq % 4 || ldk % 4 ||
+        (v && ldv % 4))
+        return DLLM_ERR_ALIGN;
+    int dev;
+    int rc = current_device(&dev);
+    if (rc) return rc;
+    RopeArgs a;
+    memset(&a, 0, sizeof(a));
+    a.q = q, a.k = k, a.v = v;
+    a.ldq = ldq, a.ldk = ldk, a.ldv = ldv;
+    a.L = L;
+    a.H = (int32_t)H, a.Hkv = (int32_t)Hkv, a.T = (int32_t)(H + Hkv * (v ? 2 : 1));
+    a.dh = (int32_t)dh, a.n_rot = (int32_t)n_rot;
+    a.pos = pos, a.turns = turns;
+    a.ms = mscale, a.eps = eps;
+    a.gq = gamma_q, a.gk = gamma_k;
+    a.oq = static_cast<__half*>(oq), a.ok = static_cast<__half*>(ok), a.ov = static_cast<__half*>(ov);
+    const int G = dh <= 64 ? 8 : dh <= 128 ? 16 : 32;
+    // Heads per CTA: one per lane group while the CTAs of all tokens fit one wave of full
+    // SMs (8 of 256 threads each), else all of a token's, whose angles are then formed once.
+    const int slots = ROPE_THREADS / G;
+    const int64_t parts = (a.T + slots - 1) / slots;
+    a.chunk = L * parts <= 8LL * g_num_sms[dev] ? slots : a.T;
+    const dim3 grid((unsigned)L, (unsigned)((a.T + a.chunk - 1) / a.chunk));
+    if (grid.y > 65535) return DLLM_ERR_ARG;
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const bool neox = layout == DLLM_ROPE_NEOX;
+    return status_of(G == 8 ? launch_rope<8>(a, grid, neox, s) : G == 16 ? launch_rope<16>(a, grid, neox, s)
+                                                                          : launch_rope<32>(a, grid, neox, s));
+}
+
+int dllm_attention_masked_workspace_bytes(int64_t Lq, int64_t Lk, int64_t H, int64_t Hkv, size_t* bytes) {
+    if (Lq < 0 || Lk < 0 || H <= 0 || Hkv <= 0 || H % Hkv || !bytes) return DLLM_ERR_ARG;
+    *bytes = 0;
+    return DLLM_OK;
+}
+
+int dllm_attention_masked(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                          int64_t Lq, int64_t Lk, int64_t H, int64_t Hkv, int64_t dh, const int32_t* kv_begin,
+                          const int32_t* kv_end, const int32_t* q_pos, float softcap, const float* slopes, void* o,
+                          dllm_ftype o_type, void* workspace, size_t workspace_bytes, dllm_stream_t stream) {
+    if (Lq < 0 || Lk < 0 || H <= 0 || Hkv <= 0 || H % Hkv || dh != ATT_DH) return DLLM_ERR_ARG;
+    if (o_type != DLLM_F32 && o_type != DLLM_F16) return DLLM_ERR_ARG;
+    if (!(softcap >= 0.0f) || !(softcap < INFINITY)) return DLLM_ERR_ARG;
+    if (Lq > (1LL << 30) || Lk > (1LL << 30) || H > 65535) return DLLM_ERR_ARG;
+    if (ldq < H * dh || ldk < Hkv * dh || ldv < Hkv * dh) return DLLM_ERR_ARG;
+    if (Lq == 0) return DLLM_OK;
+    if (!q || !o || (Lk > 0 && (!k || !v))) return DLLM_ERR_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(kv_begin) ||
+        !aligned16(kv_end) || !aligned16(q_pos) || !aligned16(slopes) || ldq % 8 || ldk % 8 || ldv % 8)
+        return DLLM_ERR_ALIGN;
+    int dev;
+    int rc = current_device(&dev);
+    if (rc) return rc;
+    (void)workspace;
+    (void)workspace_bytes;
+    MaskArgs a;
+    memset(&a, 0, sizeof(a));
+    a.q = static_cast<const __half*>(q), a.k = static_cast<const __half*>(k), a.v = static_cast<const __half*>(v);
+    a.ldq = ldq, a.ldk = ldk, a.ldv = ldv;
+    a.Lq = (int32_t)Lq, a.Lk = (int32_t)Lk, a.H = (int32_t)H, a.group = (int32_t)(H / Hkv);
+    a.kv_begin = kv_begin, a.kv_end = kv_end, a.q_pos = q_pos;
+    a.cap = softcap;
+    a.slopes = slopes;
+    a.o = o;
+    a.o_f16 = o_type == DLLM_F16;
+    return status_of(launch_pdl(attention_masked_kernel, dim3((unsigned)((Lq * H + 7) / 8)), dim3(256), 0,
+                                reinterpret_cast<cudaStream_t>(stream), a));
+}
+
+int dllm_sample(const float* logits, int64_t R, int64_t V, int64_t ldl, const float* temperature, const int32_t* top_k,
+                const float* top_p, const float* min_p, const float* u, int32_t* token, float* conf, float* entropy,
+                dllm_stream_t stream) {
+    if (R < 0 || V <= 0 || V > (1LL << 31) - 64 || ldl < V || R > (1LL << 27)) return DLLM_ERR_ARG;
+    if (R == 0) return DLLM_OK;
+    if (!logits || !token) return DLLM_ERR_ARG;
+    const void* ptrs[] = {logits, temperature, top_k, top_p, min_p, u, token, conf, entropy};
+    for (const void* p : ptrs)
+        if (!aligned16(p)) return DLLM_ERR_ALIGN;
+    int dev;
+    int rc = current_device(&dev);
+    if (rc) return rc;
+    const size_t most = 227 * 1024;
+    if (!g_sample_attr_done[dev]) {
+        if (cudaFuncSetAttribute(sample_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) != cudaSuccess)
+            return DLLM_ERR_CUDA;
+        g_sample_attr_done[dev] = true;
+    }
+    SampleArgs a;
+    memset(&a, 0, sizeof(a));
+    a.logits = logits;
+    a.V = V, a.ldl = ldl;
+    a.temperature = temperature, a.top_k = top_k, a.top_p = top_p, a.min_p = min_p, a.u = u;
+    a.token = token, a.conf = conf, a.entropy = entropy;
+    int C = 1;
+    while (C < SMP_MAX_CLUSTER && (int64_t)C * 8192 < V) C *= 2;
+    a.slice = (int32_t)round_up((V + C - 1) / C, 32);
+    const int64_t room = (int64_t)((most - sizeof(SampleShared)) / 4);
+    a.cached = (int32_t)(a.slice < room ? a.slice : room);
+    int bits = 0;
+    while ((1LL << bits) < V) bits++;
+    a.fix = 62 - bits < 51 ? 62 - bits : 51;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(C * R));
+    cfg.blockDim = dim3(SMP_THREADS);
+    cfg.dynamicSmemBytes = sizeof(SampleShared) + (size_t)a.cached * 4;
+    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)C;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return status_of(cudaLaunchKernelEx(&cfg, sample_kernel, a));
+}
+
+}  // extern "C"

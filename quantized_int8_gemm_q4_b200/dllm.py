@@ -28,6 +28,10 @@ DLLM_ERR_TIMEOUT = -6
 DLLM_ERR_WORKSPACE = -7
 DLLM_ERR_SCRATCH_LIMIT = -8
 DLLM_ERR_SCALE_RANGE = -9
+DLLM_ERR_LOGITS = -10
+DLLM_ROPE_NORM, DLLM_ROPE_NEOX = 0, 2
+DLLM_ROPE_PLAIN, DLLM_ROPE_LINEAR, DLLM_ROPE_NTK, DLLM_ROPE_YARN = 0, 1, 2, 3
+DLLM_F32, DLLM_F16 = 0, 1
 DLLM_NOALLOC_SCRATCH_BYTES = 32 << 20
 
 EXPORTS = (
@@ -36,6 +40,7 @@ EXPORTS = (
     "dllm_quantize_act",
     "dllm_rmsnorm_quantize", "dllm_swiglu_quantize",
     "dllm_qgemm_workspace_bytes", "dllm_qgemm", "dllm_qgemm_noalloc", "dllm_qkv_qgemm", "dllm_attention",
+    "dllm_rope_turns", "dllm_qk_rope", "dllm_attention_masked_workspace_bytes", "dllm_attention_masked", "dllm_sample",
     "dllm_get_device_status",
     "dllm_status_string", "dllm_debug_subblock_dots", "dllm_debug_sb_ints", "dllm_debug_bounded_wait",
     "dllm_bench_mma_i8", "dllm_debug_plan", "dllm_debug_attention_tiles",
@@ -62,7 +67,7 @@ def load() -> ctypes.CDLL:
                           "(run __graft_entry__.build() or python -m quantized_int8_gemm_q4_b200.build)")
     L = ctypes.CDLL(str(LIB_PATH))
     P, I64, I = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
-    SZ = ctypes.c_size_t
+    SZ, D = ctypes.c_size_t, ctypes.c_double
     PSZ = ctypes.POINTER(ctypes.c_size_t)
     sig = {
         "dllm_repacked_bytes": [I, I64, I64, PSZ],
@@ -79,6 +84,13 @@ def load() -> ctypes.CDLL:
         "dllm_qgemm_noalloc": [P, I, I64, I64, P, P, P, I64, P, I64, P, I64, P],
         "dllm_qkv_qgemm": [P, P, P, I, I64, I64, I64, P, P, P, I64, P, I64, P, P, I64, P, SZ, P],
         "dllm_attention": [P, P, P, I64, I64, I64, I64, I64, P, P],
+        "dllm_rope_turns": [I64, D, I, D, D, D, D, ctypes.POINTER(D), ctypes.POINTER(ctypes.c_float)],
+        "dllm_qk_rope": [P, I64, P, I64, P, I64, I64, I64, I64, I64, P, P, I64, I, ctypes.c_float, P, P,
+                         ctypes.c_float, P, P, P, P],
+        "dllm_attention_masked_workspace_bytes": [I64, I64, I64, I64, PSZ],
+        "dllm_attention_masked": [P, I64, P, I64, P, I64, I64, I64, I64, I64, I64, P, P, P, ctypes.c_float, P, P, I,
+                                  P, SZ, P],
+        "dllm_sample": [P, I64, I64, I64, P, P, P, P, P, P, P, P, P],
         "dllm_get_device_status": [P],
         "dllm_status_string": [I],
         "dllm_debug_subblock_dots": [P, I, I64, I64, P, I64, P, P],
@@ -199,6 +211,47 @@ def dllm_qkv_qgemm(wq, wk, wv, qtype: int, Nq: int, Nkv: int, K: int, q, scale, 
 def dllm_attention(q, k, v, Lq: int, Lk: int, H: int, Hkv: int, dh: int, o, stream=None):
     _check(load().dllm_attention(_ptr(q), _ptr(k), _ptr(v), Lq, Lk, H, Hkv, dh, _ptr(o), _stream(stream)),
            "dllm_attention")
+
+
+def dllm_rope_turns(n_rot: int, base: float, kind: int = DLLM_ROPE_PLAIN, factor: float = 1.0,
+                    trained_len: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """-> (turns, mscale): the float64 host tensor [n_rot / 2] of turns per position, to be copied to
+    the device once, and the factor on cos and sin."""
+    import torch
+    turns = torch.empty(max(n_rot, 0) // 2, dtype=torch.float64)
+    m = ctypes.c_float(0.0)
+    _check(load().dllm_rope_turns(n_rot, base, kind, factor, trained_len, beta_fast, beta_slow,
+                                  ctypes.cast(turns.data_ptr(), ctypes.POINTER(ctypes.c_double)), ctypes.byref(m)),
+           "dllm_rope_turns")
+    return turns, m.value
+
+
+def dllm_qk_rope(q, ldq: int, k, ldk: int, v, ldv: int, L: int, H: int, Hkv: int, dh: int, pos, turns, n_rot: int,
+                 layout: int, mscale: float, gamma_q, gamma_k, eps: float, oq, ok, ov, stream=None):
+    _check(load().dllm_qk_rope(_ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, L, H, Hkv, dh, _ptr(pos), _ptr(turns), n_rot,
+                               layout, mscale, _ptr(gamma_q), _ptr(gamma_k), eps, _ptr(oq), _ptr(ok), _ptr(ov),
+                               _stream(stream)), "dllm_qk_rope")
+
+
+def dllm_attention_masked_workspace_bytes(Lq: int, Lk: int, H: int, Hkv: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load().dllm_attention_masked_workspace_bytes(Lq, Lk, H, Hkv, ctypes.byref(out)),
+           "dllm_attention_masked_workspace_bytes")
+    return out.value
+
+
+def dllm_attention_masked(q, ldq: int, k, ldk: int, v, ldv: int, Lq: int, Lk: int, H: int, Hkv: int, dh: int,
+                          kv_begin, kv_end, q_pos, softcap: float, slopes, o, o_type: int, workspace=None,
+                          workspace_bytes: int = 0, stream=None):
+    _check(load().dllm_attention_masked(_ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, Lq, Lk, H, Hkv, dh, _ptr(kv_begin),
+                                        _ptr(kv_end), _ptr(q_pos), softcap, _ptr(slopes), _ptr(o), o_type,
+                                        _ptr(workspace), workspace_bytes, _stream(stream)), "dllm_attention_masked")
+
+
+def dllm_sample(logits, R: int, V: int, ldl: int, temperature, top_k, top_p, min_p, u, token, conf, entropy,
+                stream=None):
+    _check(load().dllm_sample(_ptr(logits), R, V, ldl, _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p),
+                              _ptr(u), _ptr(token), _ptr(conf), _ptr(entropy), _stream(stream)), "dllm_sample")
 
 
 def dllm_get_device_status(stream=None) -> int:
