@@ -1,66 +1,483 @@
-// Attention under key intervals: query i attends to the keys [kv_begin[i], kv_end[i]), with
-// an optional tanh cap on the scores and an optional bias that falls with distance.
+// Attention under key intervals on the sm_100a tensor cores: query i attends to the keys
+// [kv_begin[i], kv_end[i]), with an optional tanh cap on the scores and an optional bias
+// that falls with distance (packed documents, prefixes, blocks of a canvas over the kept
+// ones before it, windows, padding).
+//
+//   s_ij = q_i . k_j / sqrt(dh);  s = cap tanh(s / cap);  s -= slope_h |q_pos_i - j|
+//   o_i = sum over the interval of softmax(s_i)_j v_j;  an empty interval gives zeros
+//
+// A tile is 128 rows (tensor-memory lanes) of one key head: gp query heads of its group
+// (the largest divisor of the group up to 128) x 128 / gp queries, row = query * gp + head,
+// which is the order in which one TMA box of gp heads x 128 / gp rows lands in shared memory.  So
+// grouped heads read their keys once, and one query of 8 heads fills 8 rows.  A CTA has two
+// tiles (one for small grids) and the key blocks of 128 that any of their rows sees, or one of
+// `splits` equal parts of them; 12 warps:
+//   warps 0-3, 4-7  softmax of tile 0, tile 1; thread = row, all 128 scores of a block in
+//                   registers
+//   warp 8          one thread issues every MMA (S = Q K^T, O += P V; kind::f16, f32 in
+//                   tensor memory); the warp owns tensor memory
+//   warp 9, 10      TMA producers of Q and K, of V (two slots each, 128 keys x dh)
+//   warp 11         V's gate: in a block that some row does not see whole, it replaces what
+//                   is not finite by zeros and marks those keys (a weight of zero times NaN is
+//                   NaN, and the hidden key of one row is another's); a row that attends a
+//                   marked key becomes NaN
+// Issue order per block: P V of tile 0 (block kb - 1), S of tile 0 (kb), P V of tile 1, S of
+// tile 1: while one tile's softmax runs, the tensor core works on the other tile.  P lies
+// over its S in tensor memory (f16 pairs), so O_t and S_t of both tiles fill the 512 columns.
+// A commit after S(kb) also covers P V(kb - 1), so a thread that sees S may rescale O.
+//
+// Bounds per pair of tiles and block: 2048 cycles of MMA (4 x 8 of 128 x 128 x 16 at 8192
+// operations per cycle) and 2048 of the special-function unit (32768 exponentials at 16 per cycle).
 #pragma once
 #include "attention.cuh"
+#include "qgemm.cuh"
 #include "rope.cuh"
 
 namespace dllm {
 
+constexpr int MSK_MMA_WARP = 8, MSK_K_WARP = 9, MSK_V_WARP = 10, MSK_GATE_WARP = 11;
+constexpr int MSK_THREADS = 32 * 12;
+constexpr int MSK_BK = 128;  // keys per block
+// Registers per thread after setmaxnreg (softmax warpgroups; the others), out of the
+// launch's 384 x 168.
+constexpr int MSK_REG_SOFTMAX = 200, MSK_REG_OTHER = 96, MSK_REG_LAUNCH = 168;
+static_assert(256 * MSK_REG_SOFTMAX + 128 * MSK_REG_OTHER <= MSK_THREADS * MSK_REG_LAUNCH, "setmaxnreg split");
+
+struct MaskShared {
+    uint64_t q_full[2], k_full[2], v_full[2], v_ready[2], k_empty[2], v_empty[2];
+    uint64_t s_full[2], p_full[2], o_done[2], fin;
+    uint32_t tmem, flags[2][4];  // per V slot, bit j: key j's value is not finite
+    int32_t lo_min[8], hi_max[8], lo_max[8], hi_min[8];  // per softmax warp, over rows with keys
+};
+// Q x2, K x2, V x2, barriers
+constexpr size_t MSK_SMEM = 6 * (size_t)ATT_TILE + sizeof(MaskShared);
+
 struct MaskArgs {
-    const __half *q, *k, *v;
-    int64_t ldq, ldk, ldv;
     int32_t Lq, Lk, H, group;
+    int32_t gp, tq;   // heads and queries per tile
+    int32_t tiles;    // query tiles per CTA (1 or 2)
+    int32_t splits;   // parts of the key range (grid y)
     const int32_t *kv_begin, *kv_end, *q_pos;
-    float cap;
+    float cap_in, cap_out;  // s' = cap_out tanh(cap_in qk), in base-2 exponents
     const float* slopes;
     void* o;
     int32_t o_f16;
+    float* part;      // splits > 1: unnormalised O [splits][Lq][H][128]
+    float2* part_ml;  // and (m, l) [splits][Lq][H]
 };
 
-// One warp per (query, head), one online softmax over its interval; lane l holds the
-// head-dim values 4l .. 4l + 3.
-__global__ void __launch_bounds__(256) attention_masked_kernel(const __grid_constant__ MaskArgs a) {
+__device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(d)
+        : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)),
+          "l"(*reinterpret_cast<uint64_t*>(&c)));
+    return *reinterpret_cast<float2*>(&d);
+}
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(d)
+        : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+    return *reinterpret_cast<float2*>(&d);
+}
+
+// tanh(y) = 1 - 2 / (1 + 2^(2 log2(e) y)), good to a few 2^-24 absolute.
+__device__ __forceinline__ float att_tanh(float y) {
+    const float e = att_ex2(y * 2.885390081777927f);
+    return 1.0f - __fdividef(2.0f, 1.0f + e);
+}
+
+// MODE bit 0: cap, bit 1: distance bias.
+template <int MODE>
+__global__ void __launch_bounds__(MSK_THREADS, 1)
+    attention_masked_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                            const __grid_constant__ CUtensorMap tv, const __grid_constant__ MaskArgs a) {
+    constexpr bool CAP = MODE & 1, BIAS = MODE & 2;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t* const sQ = smem;                // two tiles
+    uint8_t* const sK = smem + 2 * ATT_TILE; // two slots
+    uint8_t* const sV = smem + 4 * ATT_TILE; // two slots
+    MaskShared& sh = *reinterpret_cast<MaskShared*>(smem + 6 * ATT_TILE);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // The last queries first (under causal intervals theirs are the longest), all heads of them.
+    const int n_heads = a.H / a.gp, h0 = (int)(blockIdx.x % n_heads) * a.gp, hk = h0 / a.group;
+    const int q0 = (int)((gridDim.x - 1 - blockIdx.x) / n_heads) * a.tiles * a.tq;
+    const int ntiles = a.tiles == 2 && a.Lq - q0 > a.tq ? 2 : 1;
+
+    if (threadIdx.x == 32 * MSK_MMA_WARP) {
+        for (int b = 0; b < 2; b++) {
+            mbar_init(&sh.q_full[b], 1);
+            mbar_init(&sh.k_full[b], 1);
+            mbar_init(&sh.v_full[b], 1);
+            mbar_init(&sh.v_ready[b], 1);
+            mbar_init(&sh.k_empty[b], 1);
+            mbar_init(&sh.v_empty[b], 1);
+            mbar_init(&sh.s_full[b], 1);
+            mbar_init(&sh.p_full[b], 4);
+            mbar_init(&sh.o_done[b], 1);
+        }
+        mbar_init(&sh.fin, 1);
+        fence_mbar_init();
+    }
+    if (warp == MSK_MMA_WARP) {
+        __syncwarp();
+        tmem_alloc(&sh.tmem, ATT_TM_COLS);
+        tmem_relinquish();
+    }
+    pdl_trigger();
+    pdl_wait();  // q, k, v and the intervals may come from the previous kernel on the stream
+
+    // This thread's row (softmax warps): query, head, interval.
+    const int t = warp >> 2, row = threadIdx.x & 127;
+    int qi = 0, head = 0, lo = 0, hi = 0;
+    bool live = false;
+    if (warp < 8) {
+        qi = q0 + t * a.tq + row / a.gp;
+        head = h0 + row % a.gp;
+        live = t < ntiles && row < a.tq * a.gp && qi < a.Lq;
+        if (live) {
+            lo = a.kv_begin ? max(0, __ldg(a.kv_begin + qi)) : 0;
+            hi = a.kv_end ? min(a.Lk, __ldg(a.kv_end + qi)) : a.Lk;
+        }
+        const bool some = live && lo < hi;
+        const int l0 = __reduce_min_sync(~0u, some ? lo : INT_MAX), h1 = __reduce_max_sync(~0u, some ? hi : 0);
+        const int l1 = __reduce_max_sync(~0u, some ? lo : 0), h2 = __reduce_min_sync(~0u, some ? hi : INT_MAX);
+        if (lane == 0) sh.lo_min[warp] = l0, sh.hi_max[warp] = h1, sh.lo_max[warp] = l1, sh.hi_min[warp] = h2;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = sh.tmem;
+
+    // Key blocks of each tile, and of the CTA's part of their union: [B0, B1).
+    int t0[2], t1[2], b_full0 = 0, b_full1 = INT_MAX;  // keys every row of the CTA sees
+#pragma unroll
+    for (int x = 0; x < 2; x++) {
+        int l = INT_MAX, h = 0;
+#pragma unroll
+        for (int w = 4 * x; w < 4 * x + 4; w++) {
+            l = min(l, sh.lo_min[w]);
+            h = max(h, sh.hi_max[w]);
+            b_full0 = max(b_full0, sh.lo_max[w]);
+            b_full1 = min(b_full1, sh.hi_min[w]);
+        }
+        t0[x] = l < h ? l / MSK_BK : 0;
+        t1[x] = l < h ? (h + MSK_BK - 1) / MSK_BK : 0;
+    }
+    int B0 = t0[0] < t1[0] ? (t0[1] < t1[1] ? min(t0[0], t0[1]) : t0[0]) : t0[1], B1 = max(t1[0], t1[1]);
+    if (a.splits > 1) {
+        const int n = (B1 - B0 + a.splits - 1) / a.splits;
+        B0 = min(B1, B0 + (int)blockIdx.y * n);
+        B1 = min(B1, B0 + n);
+    }
+#pragma unroll
+    for (int x = 0; x < 2; x++) t0[x] = max(t0[x], B0), t1[x] = min(t1[x], B1);  // empty where t0 >= t1
+    // A block that every row of both tiles sees whole needs no gate.
+    auto whole = [&](int kb) { return kb * MSK_BK >= b_full0 && (kb + 1) * MSK_BK <= b_full1; };
+
+    if (warp >= 8) {
+        setmaxnreg_dec<MSK_REG_OTHER>();
+        if (warp == MSK_K_WARP || warp == MSK_V_WARP) {
+            // ------------------------------------------------------------ TMA producers
+            const bool is_k = warp == MSK_K_WARP;
+            const uint32_t q_bytes = (uint32_t)(a.gp * a.tq) * ATT_DH * 2;
+            const int nq = is_k && B0 < B1 ? ntiles : 0;
+            for (int x = 0; x < nq; x++) {
+                if (lane == 0) mbar_arrive_expect_tx(&sh.q_full[x], q_bytes);
+                __syncwarp();
+                att_tma_tile(sQ + x * ATT_TILE, &tq, h0, q0 + x * a.tq, &sh.q_full[x], lane);
+            }
+            uint64_t* const full = is_k ? sh.k_full : sh.v_full;
+            uint64_t* const empty = is_k ? sh.k_empty : sh.v_empty;
+            const CUtensorMap* const tmap = is_k ? &tk : &tv;
+            uint8_t* const dst = is_k ? sK : sV;
+            int n = 0;
+            for (; n < B1 - B0; n++) {
+                const int b = n & 1;
+                if (n >= 2 && !__all_sync(~0u, att_wait(&empty[b], ((n >> 1) - 1) & 1))) break;
+                if (lane == 0) mbar_arrive_expect_tx(&full[b], ATT_TILE);
+                __syncwarp();
+                att_tma_tile(dst + b * ATT_TILE, tmap, hk, (B0 + n) * MSK_BK, &full[b], lane);
+            }
+            // No copy may still be landing when the CTA exits, also when a wait ran out.
+            if (lane == 0) {
+                for (int m = n > 2 ? n - 2 : 0; m < n; m++) drain_wait(&full[m & 1], (m >> 1) & 1);
+                for (int x = 0; x < nq; x++) drain_wait(&sh.q_full[x], 0);
+            }
+            __syncwarp();
+        } else if (warp == MSK_GATE_WARP) {
+            // ------------------------------------------------------------ V's gate
+            for (int n = 0; n < B1 - B0; n++) {
+                const int b = n & 1;
+                if (!__all_sync(~0u, att_wait(&sh.v_full[b], (n >> 1) & 1))) break;
+                if (!whole(B0 + n)) {
+                    if (lane < 4) sh.flags[b][lane] = 0;
+                    __syncwarp();
+                    uint4* const v = reinterpret_cast<uint4*>(sV + b * ATT_TILE);
+#pragma unroll 8
+                    for (int i = lane; i < ATT_TILE / 16; i += 32) {
+                        const uint4 x = v[i];
+                        // an f16 with all exponent bits set carries into its sign bit
+                        auto c = [](uint32_t y) { return (y & 0x7fff7fffu) + 0x04000400u; };
+                        if ((c(x.x) | c(x.y) | c(x.z) | c(x.w)) & 0x80008000u) {
+                            auto z = [&](uint32_t y) {
+                                const uint32_t m = (c(y) & 0x80008000u) >> 15;  // 1 per half to clear
+                                return y & ~(m * 0xffffu);
+                            };
+                            v[i] = make_uint4(z(x.x), z(x.y), z(x.z), z(x.w));
+                            const int key = (i >> 3) & 127;  // 128-byte rows of 64 head-dim values
+                            atomicOr(&sh.flags[b][key >> 5], 1u << (key & 31));
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                if (lane == 0) mbar_arrive(&sh.v_ready[b]);
+            }
+        } else if (lane == 0) {
+            // ------------------------------------------------------------ MMA issue
+            constexpr uint32_t ID_S = idesc_f16(128, MSK_BK);
+            constexpr uint32_t ID_O = idesc_f16(128, ATT_DH) | (1u << 16);  // B (V) MN-major
+            const uint64_t dq = att_qk_desc(sQ), dk = att_qk_desc(sK), dv = att_v_desc(sV);
+            bool ok = true;
+            // One step beyond the last block: its P V only.
+            for (int n = 0; ok && n <= B1 - B0; n++) {
+                const int kb = B0 + n, b = n & 1;
+#pragma unroll 1
+                for (int x = 0; ok && x < 2; x++) {
+                    const uint32_t tO = tm + 256 * x, tS = tO + 128;
+                    if (n > 0 && kb - 1 >= t0[x] && kb - 1 < t1[x]) {
+                        const int p = b ^ 1;  // slot of block kb - 1
+                        ok = att_wait(&sh.p_full[x], (kb - 1 - t0[x]) & 1) && att_wait(&sh.v_ready[p], ((n - 1) >> 1) & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t d = dv + (uint64_t)(p * (ATT_TILE >> 4));
+                        mma_f16_ts(tO, tS, d, ID_O, kb - 1 > t0[x]);
+#pragma unroll
+                        for (int kk = 1; kk < MSK_BK / 16; kk++) mma_f16_ts(tO, tS + 8 * kk, d + att_v_step(kk), ID_O, 1);
+                        if (kb == t1[x]) tc_commit(&sh.o_done[x]);
+                    }
+                    if (kb >= t0[x] && kb < t1[x]) {
+                        ok = (kb > t0[x] || att_wait(&sh.q_full[x], 0)) && att_wait(&sh.k_full[b], (n >> 1) & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t q = dq + (uint64_t)(x * (ATT_TILE >> 4)), d = dk + (uint64_t)(b * (ATT_TILE >> 4));
+                        mma_f16_ss(tS, q, d, ID_S, 0);
+#pragma unroll
+                        for (int kk = 1; kk < ATT_DH / 16; kk++)
+                            mma_f16_ss(tS, q + att_qk_step(kk), d + att_qk_step(kk), ID_S, 1);
+                        tc_commit(&sh.s_full[x]);
+                    }
+                }
+                if (ok && n > 0) {
+                    // a block that no tile multiplied still passes its gate before its slot is refilled
+                    ok = att_wait(&sh.v_ready[b ^ 1], ((n - 1) >> 1) & 1);
+                    tc_commit(&sh.v_empty[b ^ 1]);
+                }
+                if (ok && kb < B1) {
+                    ok = att_wait(&sh.k_full[b], (n >> 1) & 1);
+                    tc_commit(&sh.k_empty[b]);
+                }
+            }
+            // Every MMA issued above completes before tensor memory is released.
+            tc_commit(&sh.fin);
+            drain_wait(&sh.fin, 0);
+        }
+        __syncwarp();
+    } else {
+        // ---------------------------------------------------------------- softmax, output
+        setmaxnreg_inc<MSK_REG_SOFTMAX>();
+        const uint32_t tO = tm + ((uint32_t)(32 * (warp & 3)) << 16) + 256 * t, tS = tO + 128;
+        const int w_lo0 = sh.lo_min[warp], w_hi1 = sh.hi_max[warp], w_lo1 = sh.lo_max[warp], w_hi0 = sh.hi_min[warp];
+        const bool some = lo < hi;
+        if (!some) lo = 0, hi = a.Lk;  // a row without keys runs along; it stores zeros
+        float slope = 0.0f;
+        int qp = 0;
+        if (BIAS && live) {
+            slope = __ldg(a.slopes + head) * 1.4426950408889634f;
+            qp = a.q_pos ? __ldg(a.q_pos + qi) : qi + a.Lk - a.Lq;
+        }
+        float m = -INFINITY, l = 0.0f;
+        bool ok = true;
+        for (int kb = t0[t]; kb < t1[t]; kb++) {
+            ok = __all_sync(~0u, att_wait(&sh.s_full[t], (kb - t0[t]) & 1));
+            if (!ok) break;
+            tc_fence_after();
+            const int k0 = kb * MSK_BK;
+            if (k0 >= w_hi1 || k0 + MSK_BK <= w_lo0) {  // no row of the warp sees the block
+                uint32_t z[16];
+#pragma unroll
+                for (int e = 0; e < 16; e++) z[e] = 0u;
+#pragma unroll
+                for (int c = 0; c < 4; c++) tmem_st16(tS + 16 * c, z);
+            } else {
+                float s[MSK_BK];
+#pragma unroll
+                for (int c = 0; c < 8; c++) tmem_ld16(tS + 16 * c, reinterpret_cast<uint32_t*>(s) + 16 * c);
+                tmem_wait_ld();
+                if constexpr (CAP) {
+#pragma unroll
+                    for (int j = 0; j < MSK_BK; j++) s[j] = a.cap_out * att_tanh(s[j] * a.cap_in);
+                } else if constexpr (BIAS) {
+#pragma unroll
+                    for (int j = 0; j < MSK_BK; j++) s[j] *= ATT_C;
+                }
+                if constexpr (BIAS) {
+                    const float d = (float)((int64_t)qp - k0);
+#pragma unroll
+                    for (int j = 0; j < MSK_BK; j++) s[j] = fmaf(-slope, fabsf(d - (float)j), s[j]);
+                }
+                if (k0 < w_lo1 || k0 + MSK_BK > w_hi0) {  // warp-uniform: some row hides some key
+                    const int from = lo - k0, n = hi - lo;
+#pragma unroll
+                    for (int j = 0; j < MSK_BK; j++)
+                        if ((uint32_t)(j - from) >= (uint32_t)n) s[j] = -INFINITY;
+                }
+                if (!whole(kb)) {  // the gate has looked at V: a marked key of the row's own?
+                    const int b = (kb - B0) & 1;
+                    ok = __all_sync(~0u, att_wait(&sh.v_ready[b], ((kb - B0) >> 1) & 1));
+                    if (!ok) break;
+#pragma unroll 1
+                    for (int w = 0; w < 4; w++)
+                        for (uint32_t f = sh.flags[b][w]; f; f &= f - 1)
+                            if ((uint32_t)(k0 + 32 * w + __ffs(f) - 1 - lo) < (uint32_t)(hi - lo)) l = NAN;
+                }
+                float mx[8];
+#pragma unroll
+                for (int e = 0; e < 8; e++) mx[e] = s[e];
+#pragma unroll
+                for (int j = 8; j < MSK_BK; j += 16)
+#pragma unroll
+                    for (int e = 0; e < 8; e++)
+                        mx[e] = j + 8 + e < MSK_BK ? max3f(mx[e], s[j + e], s[j + 8 + e]) : fmaxf(mx[e], s[j + e]);
+                float top = max3f(max3f(mx[0], mx[1], mx[2]), max3f(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+                constexpr float C = CAP || BIAS ? 1.0f : ATT_C;
+                top *= C;
+                const bool raise = top > m + ATT_RESCALE_LOG2;  // also from -inf; not where all is hidden
+                if (__any_sync(~0u, raise)) {
+                    // S(kb) is committed after P V(kb - 1): O is complete
+                    const float alpha = raise ? att_ex2(m - top) : 1.0f;  // 0 from -inf
+                    if (raise) m = top;
+                    l *= alpha;
+                    if (kb > t0[t]) {
+#pragma unroll 1
+                        for (int c = 0; c < 8; c++) {
+                            uint32_t r[16];
+                            tmem_ld16(tO + 16 * c, r);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 16; e++) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
+                            tmem_st16(tO + 16 * c, r);
+                        }
+                    }
+                }
+                const float neg = m == -INFINITY ? 0.0f : -m;
+                const float2 c2 = make_float2(C, C), n2 = make_float2(neg, neg);
+                float2 sum[4];
+#pragma unroll
+                for (int e = 0; e < 4; e++) sum[e] = make_float2(0.0f, 0.0f);
+#pragma unroll
+                for (int c = 0; c < 4; c++) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int e = 0; e < 16; e++) {
+                        float2 x = make_float2(s[32 * c + 2 * e], s[32 * c + 2 * e + 1]);
+                        x = CAP || BIAS ? fadd2(x, n2) : ffma2(x, c2, n2);
+                        x.x = att_ex2(x.x);
+                        x.y = att_ex2(x.y);
+                        sum[e & 3] = fadd2(sum[e & 3], x);
+                        pk[e] = pack_h2(x.x, x.y);
+                    }
+                    tmem_st16(tS + 16 * c, pk);
+                }
+                const float2 u = fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3]));
+                l += u.x + u.y;
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.p_full[t]);
+        }
+        const bool ran = t0[t] < t1[t];
+        if (ran && ok) ok = __all_sync(~0u, att_wait(&sh.o_done[t], 0));
+        if (ok) {
+            tc_fence_after();
+            const int64_t at = (int64_t)qi * a.H + head;
+            const bool split = a.splits > 1;
+            const int64_t pat = (int64_t)blockIdx.y * a.Lq * a.H + at;
+            const float inv = some && ran ? (split ? 1.0f : 1.0f / l) : 0.0f;
+            if (split && live) a.part_ml[pat] = some && ran ? make_float2(m, l) : make_float2(-INFINITY, 0.0f);
+#pragma unroll 1
+            for (int c = 0; c < 8; c++) {
+                float r[16];
+                if (ran) {
+                    tmem_ld16(tO + 16 * c, reinterpret_cast<uint32_t*>(r));
+                    tmem_wait_ld();
+                }
+#pragma unroll
+                for (int e = 0; e < 16; e++) r[e] = some && ran ? r[e] * inv : 0.0f;
+                if (!live || (split && !ran)) continue;
+                if (split || !a.o_f16) {
+                    float* dst = split ? a.part + pat * ATT_DH : static_cast<float*>(a.o) + at * ATT_DH;
+#pragma unroll
+                    for (int e = 0; e < 4; e++)
+                        reinterpret_cast<float4*>(dst + 16 * c)[e] =
+                            make_float4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
+                } else {
+                    __half* dst = static_cast<__half*>(a.o) + at * ATT_DH;
+#pragma unroll
+                    for (int e = 0; e < 2; e++)
+                        reinterpret_cast<uint4*>(dst + 16 * c)[e] =
+                            make_uint4(pack_h2(r[8 * e], r[8 * e + 1]), pack_h2(r[8 * e + 2], r[8 * e + 3]),
+                                       pack_h2(r[8 * e + 4], r[8 * e + 5]), pack_h2(r[8 * e + 6], r[8 * e + 7]));
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == MSK_MMA_WARP) {
+        tc_fence_after();
+        tmem_dealloc(tm, ATT_TM_COLS);
+    }
+}
+
+// Joins the parts of the key range: o = sum_z 2^(m_z - M) O_z / sum_z 2^(m_z - M) l_z, one
+// warp per (query, head); no key at all (every m -inf) gives zeros.
+__global__ void __launch_bounds__(128) attention_masked_join_kernel(const float* __restrict__ part,
+                                                                    const float2* __restrict__ ml, int64_t rows,
+                                                                    int splits, void* __restrict__ o, int o_f16) {
     pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x & 31;
-    const int64_t g = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (g >= (int64_t)a.Lq * a.H) return;
-    const int i = (int)(g / a.H), h = (int)(g % a.H), hk = h / a.group;
-    const int lo = a.kv_begin ? max(0, a.kv_begin[i]) : 0, hi = a.kv_end ? min(a.Lk, a.kv_end[i]) : a.Lk;
-    const int qp = a.q_pos ? a.q_pos[i] : i + a.Lk - a.Lq;
-    auto load4 = [&](const __half* p, float (&x)[4]) {
-        const uint2 u = *reinterpret_cast<const uint2*>(p + 4 * lane);
-        const float2 s = __half22float2(*reinterpret_cast<const __half2*>(&u.x)),
-                     t = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
-        x[0] = s.x, x[1] = s.y, x[2] = t.x, x[3] = t.y;
-    };
-    float q[4], acc[4] = {0, 0, 0, 0}, m = -INFINITY, l = 0.0f;
-    load4(a.q + i * a.ldq + h * 128, q);
-    const float slope = a.slopes ? a.slopes[h] : 0.0f;
-    for (int j = lo; j < hi; j++) {
-        float x[4];
-        load4(a.k + j * a.ldk + hk * 128, x);
-        float s = q[0] * x[0] + q[1] * x[1] + q[2] * x[2] + q[3] * x[3];
+    const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (at >= rows) return;
+    float M = -INFINITY;
+    for (int z = lane; z < splits; z += 32) M = fmaxf(M, ml[z * rows + at].x);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
-        s *= 0.08838834764831845f;
-        if (a.cap > 0.0f) s = a.cap * tanhf(s / a.cap);
-        if (a.slopes) s -= slope * fabsf((float)qp - (float)j);
-        const float mn = fmaxf(m, s), c = expf(m - mn), p = expf(s - mn);
-        load4(a.v + j * a.ldv + hk * 128, x);
-        l = l * c + p;
-#pragma unroll
-        for (int e = 0; e < 4; e++) acc[e] = acc[e] * c + p * x[e];
-        m = mn;
+    for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, d));
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float l = 0.0f;
+    for (int z = 0; z < splits; z++) {
+        const float2 x = ml[z * rows + at];
+        if (x.x == -INFINITY) continue;
+        const float w = att_ex2(x.x - M);
+        const float4 p = reinterpret_cast<const float4*>(part + (z * rows + at) * ATT_DH)[lane];
+        l = fmaf(w, x.y, l);
+        acc.x = fmaf(w, p.x, acc.x);
+        acc.y = fmaf(w, p.y, acc.y);
+        acc.z = fmaf(w, p.z, acc.z);
+        acc.w = fmaf(w, p.w, acc.w);
     }
-    const float inv = lo < hi ? 1.0f / l : 0.0f;
-    const int64_t at = g * 128 + 4 * lane;
-    if (a.o_f16)
-        *reinterpret_cast<uint2*>(static_cast<__half*>(a.o) + at) =
-            make_uint2(pack_h2(acc[0] * inv, acc[1] * inv), pack_h2(acc[2] * inv, acc[3] * inv));
+    const float inv = M == -INFINITY ? 0.0f : 1.0f / l;
+    if (o_f16)
+        reinterpret_cast<uint2*>(static_cast<__half*>(o) + at * ATT_DH)[lane] =
+            make_uint2(pack_h2(acc.x * inv, acc.y * inv), pack_h2(acc.z * inv, acc.w * inv));
     else
-        *reinterpret_cast<float4*>(static_cast<float*>(a.o) + at) =
-            make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
+        reinterpret_cast<float4*>(static_cast<float*>(o) + at * ATT_DH)[lane] =
+            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
 }
 
 }  // namespace dllm

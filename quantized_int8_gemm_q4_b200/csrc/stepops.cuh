@@ -26,6 +26,70 @@ int status_of(cudaError_t e) {
     return launch_status();
 }
 
+// A [rows][heads][128] f16 tensor with rows `ld` values apart as the 3-D tensor (head dim,
+// head, row), 128-byte swizzled boxes of 64 head-dim values.  Encoded on every call: a map
+// kept by address would outlive the buffer it describes.
+bool encode_rows(CUtensorMap* m, const void* base, int64_t rows, int64_t heads, int64_t ld, int box_heads,
+                 int box_rows) {
+    const EncodeTiledFn fn = encode_tiled();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)ATT_DH, (cuuint64_t)heads, (cuuint64_t)rows};
+    const cuuint64_t strides[2] = {(cuuint64_t)ATT_DH * 2, (cuuint64_t)(ld * 2)};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct MaskPlan {
+    int gp, tq, tiles, splits;
+    int64_t grid;
+    size_t ml_off, bytes;
+};
+
+// Tiles, CTAs and key parts of a masked attention call.  Two query tiles per CTA once one
+// each would need more than one wave; with at most half a wave of CTAs the keys are cut
+// into parts of at least two blocks, up to one wave in all.
+MaskPlan mask_plan(int64_t Lq, int64_t Lk, int64_t H, int64_t Hkv, int sms) {
+    MaskPlan p;
+    const int group = (int)(H / Hkv);
+    p.gp = group < 128 ? group : 128;
+    while (group % p.gp) p.gp--;
+    p.tq = 128 / p.gp;
+    const int64_t n_heads = H / p.gp, n_tiles = (Lq + p.tq - 1) / p.tq, blocks = (Lk + MSK_BK - 1) / MSK_BK;
+    p.tiles = n_tiles * n_heads > sms ? 2 : 1;
+    p.grid = (n_tiles + p.tiles - 1) / p.tiles * n_heads;
+    p.splits = 1;
+    if (2 * p.grid <= sms && blocks >= 4) {
+        const int64_t most = sms / p.grid;
+        p.splits = (int)(most < blocks / 2 ? most : blocks / 2);
+    }
+    p.ml_off = p.bytes = 0;
+    if (p.splits > 1) {
+        p.ml_off = align256((size_t)p.splits * Lq * H * ATT_DH * 4);
+        p.bytes = p.ml_off + align256((size_t)p.splits * Lq * H * 8);
+    }
+    return p;
+}
+
+bool g_mask_attr_done[MAX_DEV];
+
+template <int MODE>
+bool mask_attribute() {
+    cudaFuncAttributes fa;
+    return cudaFuncSetAttribute(attention_masked_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)MSK_SMEM) == cudaSuccess &&
+           cudaFuncGetAttributes(&fa, attention_masked_kernel<MODE>) == cudaSuccess &&
+           fa.numRegs >= MSK_REG_LAUNCH;  // the warpgroups' setmaxnreg split must fit in the launch's registers
+}
+
+bool mask_attributes(int dev) {
+    if (!g_mask_attr_done[dev])
+        g_mask_attr_done[dev] = mask_attribute<0>() && mask_attribute<1>() && mask_attribute<2>() && mask_attribute<3>();
+    return g_mask_attr_done[dev];
+}
+
 }  // namespace
 
 extern "C" {
@@ -117,8 +181,12 @@ int dllm_qk_rope(const float* q, int64_t ldq, const float* k, int64_t ldk, const
 }
 
 int dllm_attention_masked_workspace_bytes(int64_t Lq, int64_t Lk, int64_t H, int64_t Hkv, size_t* bytes) {
-    if (Lq < 0 || Lk < 0 || H <= 0 || Hkv <= 0 || H % Hkv || !bytes) return DLLM_ERR_ARG;
-    *bytes = 0;
+    if (Lq < 0 || Lk < 0 || Lq > (1LL << 30) || Lk > (1LL << 30) || H <= 0 || H > 65535 || Hkv <= 0 || H % Hkv || !bytes)
+        return DLLM_ERR_ARG;
+    int dev;
+    int rc = current_device(&dev);
+    if (rc) return rc;
+    *bytes = mask_plan(Lq, Lk, H, Hkv, g_num_sms[dev]).bytes;
     return DLLM_OK;
 }
 
@@ -131,28 +199,50 @@ int dllm_attention_masked(const void* q, int64_t ldq, const void* k, int64_t ldk
     if (!(softcap >= 0.0f) || !(softcap < INFINITY)) return DLLM_ERR_ARG;
     if (Lq > (1LL << 30) || Lk > (1LL << 30) || H > 65535) return DLLM_ERR_ARG;
     if (ldq < H * dh || ldk < Hkv * dh || ldv < Hkv * dh) return DLLM_ERR_ARG;
+    if (ldq >= (1LL << 39) || ldk >= (1LL << 39) || ldv >= (1LL << 39)) return DLLM_ERR_ARG;  // tensor-map strides
     if (Lq == 0) return DLLM_OK;
     if (!q || !o || (Lk > 0 && (!k || !v))) return DLLM_ERR_ARG;
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(kv_begin) ||
-        !aligned16(kv_end) || !aligned16(q_pos) || !aligned16(slopes) || ldq % 8 || ldk % 8 || ldv % 8)
+        !aligned16(kv_end) || !aligned16(q_pos) || !aligned16(slopes) || !aligned16(workspace) || ldq % 8 || ldk % 8 ||
+        ldv % 8)
         return DLLM_ERR_ALIGN;
     int dev;
     int rc = current_device(&dev);
     if (rc) return rc;
-    (void)workspace;
-    (void)workspace_bytes;
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (Lk == 0)
+        return status_of(cudaMemsetAsync(o, 0, (size_t)(Lq * H * dh) * (o_type == DLLM_F16 ? 2 : 4), s));
+    const MaskPlan p = mask_plan(Lq, Lk, H, Hkv, g_num_sms[dev]);
+    if (p.grid > (1LL << 31) - 1) return DLLM_ERR_ARG;
+    if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes)) return DLLM_ERR_WORKSPACE;
+    if (!mask_attributes(dev)) return DLLM_ERR_CUDA;
+    CUtensorMap tq, tk, tv;
+    if (!encode_rows(&tq, q, Lq, H, ldq, p.gp, p.tq) || !encode_rows(&tk, k, Lk, Hkv, ldk, 1, MSK_BK) ||
+        !encode_rows(&tv, v, Lk, Hkv, ldv, 1, MSK_BK))
+        return DLLM_ERR_CUDA;
     MaskArgs a;
     memset(&a, 0, sizeof(a));
-    a.q = static_cast<const __half*>(q), a.k = static_cast<const __half*>(k), a.v = static_cast<const __half*>(v);
-    a.ldq = ldq, a.ldk = ldk, a.ldv = ldv;
     a.Lq = (int32_t)Lq, a.Lk = (int32_t)Lk, a.H = (int32_t)H, a.group = (int32_t)(H / Hkv);
+    a.gp = p.gp, a.tq = p.tq, a.tiles = p.tiles, a.splits = p.splits;
     a.kv_begin = kv_begin, a.kv_end = kv_end, a.q_pos = q_pos;
-    a.cap = softcap;
+    const double scale = 0.08838834764831844, log2e = 1.4426950408889634;  // 1 / sqrt(128)
+    a.cap_in = softcap > 0.0f ? (float)(scale / softcap) : 0.0f;
+    a.cap_out = (float)(softcap * log2e);
     a.slopes = slopes;
     a.o = o;
     a.o_f16 = o_type == DLLM_F16;
-    return status_of(launch_pdl(attention_masked_kernel, dim3((unsigned)((Lq * H + 7) / 8)), dim3(256), 0,
-                                reinterpret_cast<cudaStream_t>(stream), a));
+    a.part = static_cast<float*>(workspace);
+    a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + p.ml_off);
+    const dim3 grid((unsigned)p.grid, (unsigned)p.splits);
+    const int mode = (softcap > 0.0f ? 1 : 0) + (slopes ? 2 : 0);
+    const auto kernel = mode == 0   ? attention_masked_kernel<0>
+                        : mode == 1 ? attention_masked_kernel<1>
+                        : mode == 2 ? attention_masked_kernel<2>
+                                    : attention_masked_kernel<3>;
+    rc = status_of(launch_pdl(kernel, grid, dim3(MSK_THREADS), MSK_SMEM, s, tq, tk, tv, a));
+    if (rc || p.splits == 1) return rc;
+    return status_of(launch_pdl(attention_masked_join_kernel, dim3((unsigned)((Lq * H + 3) / 4)), dim3(128), 0, s, a.part,
+                                a.part_ml, Lq * H, p.splits, o, a.o_f16));
 }
 
 int dllm_sample(const float* logits, int64_t R, int64_t V, int64_t ldl, const float* temperature, const int32_t* top_k,
