@@ -270,9 +270,9 @@ int dllm_sample(const float* logits, int64_t R, int64_t V, int64_t ldl, const fl
     a.temperature = temperature, a.top_k = top_k, a.top_p = top_p, a.min_p = min_p, a.u = u;
     a.token = token, a.conf = conf, a.entropy = entropy;
     int C = 1;
-    while (C < SMP_MAX_CLUSTER && (int64_t)C * 8192 < V) C *= 2;
-    a.slice = (int32_t)round_up((V + C - 1) / C, 32);
-    const int64_t room = (int64_t)((most - sizeof(SampleShared)) / 4);
+    while (C < 8 && (int64_t)C * 8192 < V) C *= 2;
+    a.slice = (int32_t)round_up((V + 3 + C - 1) / C, 128);
+    const int64_t room = (int64_t)((most - sizeof(SampleShared)) / 16 * 4);
     a.cached = (int32_t)(a.slice < room ? a.slice : room);
     int bits = 0;
     while ((1LL << bits) < V) bits++;
