@@ -28,6 +28,8 @@
 #pragma once
 #include <cooperative_groups.h>
 
+#include <cfloat>
+
 #include "layout.cuh"
 
 namespace dllm {
@@ -36,7 +38,7 @@ constexpr int SMP_THREADS = 512;
 constexpr int SMP_WARPS = SMP_THREADS / 32;
 constexpr int SMP_BINS = 2048;
 constexpr int SMP_COARSE = SMP_BINS / 32;
-constexpr int SMP_LIST = SMP_THREADS;  // elements ranked exactly, one per thread
+constexpr int SMP_LIST = SMP_THREADS / 2;  // elements ranked exactly
 constexpr int SMP_MAX_CLUSTER = 16;
 constexpr int SMP_TABLE = 256;
 constexpr int ERR_LOGITS = -10;
@@ -62,20 +64,24 @@ struct alignas(16) SampleShared {  // the slice follows it, read in 16-byte vect
     uint32_t ccnt[SMP_MAX_CLUSTER][SMP_COARSE];          // every CTA's coarse sums
     u64 cmass[SMP_MAX_CLUSTER][SMP_COARSE];
     u64 before_c[SMP_COARSE + 1], before_m[SMP_COARSE + 1];  // the cluster's, before each coarse bin
-    u64 lcode[SMP_LIST], lw[SMP_LIST];                   // the gathered bin: order code, weight
+    u64 mine[2][SMP_LIST];                               // this CTA's elements of a gathered bin: order codes
+    u64 lcode[SMP_LIST], lw[SMP_LIST];                   // all of them, and their weights
     u64 box[2][4][SMP_MAX_CLUSTER];                      // one exchange: words of every CTA
+    u64 plain[3][SMP_MAX_CLUSTER];                       // every CTA's sums of the plain softmax
     u64 red[4][SMP_WARPS];
-    u64 found[3], kept_mass;  // crossing bin: count before, mass before, its count; mass up to the cut
-    double table[SMP_TABLE];  // 2^(i / 256)
-    uint32_t found_bin, n_list, best;
+    u64 found[2], kept_mass;  // crossing bin: count before, mass before; mass up to the cut
+    double table[SMP_TABLE];  // 2^(fix + i / 256)
+    uint32_t found_bin, found_upto, n_mine[2], n_list, best;
     u64 cut;                  // order code
+    uint64_t landed;          // mbarrier: the slice is in shared memory
+    double scale, ln_min_p;   // log2(e) / T, ln(min_p)
 };
 
 static_assert(sizeof(SampleShared) % 16 == 0, "the slice behind it is read as float4");
 
-// Order-preserving code of a float (which is not -0): larger value, larger code.
+// Order-preserving code of a float (-0 counts as +0): larger value, larger code.
 __device__ __forceinline__ uint32_t smp_key(float x) {
-    const uint32_t b = __float_as_uint(x);
+    const uint32_t b = __float_as_uint(x + 0.0f);
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 __device__ __forceinline__ float smp_value(uint32_t k) {
@@ -101,30 +107,40 @@ __device__ __forceinline__ double smp_warp_sum(double v) {
     return v;
 }
 
+__device__ __forceinline__ SampleShared& smp_shared() {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    return *reinterpret_cast<SampleShared*>(smem);
+}
+__device__ __forceinline__ float* smp_cache() {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    return reinterpret_cast<float*>(smem + sizeof(SampleShared));
+}
+
 // One row, as one CTA of its cluster sees it.
 struct SampleRow {
     cooperative_groups::cluster_group cl;
-    SampleShared& sm;
     const float* src;   // row in global memory
-    float* cache;
     int64_t V;
     int C, r, w, lane;  // CTAs, this one's rank; warp, lane
     int n, cached;      // elements of the slice (a multiple of 4), and of them in shared memory
     int64_t first;      // row index of the slice's first element (before the row: filled with -inf)
     float top;          // largest logit
-    double scale;       // log2(e) / T
-    double least;       // base-2 exponents below it round to weight 0
-    double min_w;       // 2^fix * min_p
-    int fix;
-    float cut_val;      // kept: above, or equal and not behind cut_idx
-    uint32_t cut_idx;
-    int phase;
+    double topd, scale; // it widened; log2(e) / T
+    float lowest;       // weighs less than half a unit, or is the lowest float
+    bool coarse;
+    double floor_t;     // base-2 exponent that rounds to weight 0
+    u64 min_w;          // min_p in fixed point
+    float cut_val;      // kept: above, or equal and not behind cut_i
+    int cut_i;
+    int phase;          // which box comes next
     // the present histogram: values [vmin, vmax], spread evenly by value or by code
     float vmin, vmax, vhi, inv;
+    float low_val;      // the higher of vmin and the cut
+    int low_i;
     int shift;
     bool linear;
 
-    // Four elements; outside the row -inf.  -0 becomes +0.
+    // Four elements; outside the row -inf.
     __device__ __forceinline__ float4 load4(int i) const {
         const int64_t g = first + i;
         float4 x;
@@ -136,56 +152,97 @@ struct SampleRow {
             x.z = g + 2 >= 0 && g + 2 < V ? __ldg(src + g + 2) : -INFINITY;
             x.w = g + 3 >= 0 && g + 3 < V ? __ldg(src + g + 3) : -INFINITY;
         }
-        return make_float4(x.x + 0.0f, x.y + 0.0f, x.z + 0.0f, x.w + 0.0f);
+        return x;
     }
-    __device__ __forceinline__ float4 at4(int i) const {
-        return i < cached ? *reinterpret_cast<const float4*>(cache + i) : load4(i);
+    // f(x, i) for the elements lo + 4 k .. lo + 4 k + 3 of [lo, hi), k = first thread, + step ...;
+    // two loads are in flight.
+    template <typename F>
+    __device__ __forceinline__ void each(int lo, int hi, int thread, int threads, F f) const {
+        const float* const cache = smp_cache();
+        const int step = 4 * threads, end = min(hi, cached);
+        int i = lo + 4 * thread;
+        for (; i + step < end; i += 2 * step) {
+            const float4 x = *reinterpret_cast<const float4*>(cache + i);
+            const float4 y = *reinterpret_cast<const float4*>(cache + i + step);
+            f(x, i);
+            f(y, i + step);
+        }
+        for (; i < end; i += step) f(*reinterpret_cast<const float4*>(cache + i), i);
+        for (; i < hi; i += step) f(load4(i), i);
     }
-    __device__ __forceinline__ uint32_t index(int i) const { return (uint32_t)(first + i); }
+    __device__ __forceinline__ uint32_t index(int i) const { return (uint32_t)first + (uint32_t)i; }
 
-    // Fixed-point weight of a logit, 0 below min_p: 2^t by table and polynomial (Tang 1989),
-    // t = k + j / 256 + f, |f| <= 2^-9, the polynomial's next term below 2^-54.  Adding
-    // 1.5 2^44 rounds t to a multiple of 1/256 and leaves 256 k + j in the low word; adding
-    // 2^52 to the weight times 2^fix rounds it to a whole number, held by the low mantissa.
-    __device__ __forceinline__ u64 weight(float l) const {
-        const double t = ((double)l - (double)top) * scale;
-        if (!(t > least)) return 0;
+    // Fixed-point weight of a logit: 2^t by table and polynomial (Tang 1989), t = k + j / 256 + f,
+    // |f| <= 2^-9, the polynomial's next term below 2^-54.  Adding 1.5 2^44 rounds t to a
+    // multiple of 1/256 and leaves 256 k + j in the low word; adding 2^52 to the weight (the
+    // table holds 2^(fix + j / 256)) rounds it to a whole number, held by the low mantissa.
+    __device__ __forceinline__ u64 weight_of(double t) const {
         const double tm = t + 26388279066624.0;
         const int kj = __double2loint(tm);
         const double f = t - (tm - 26388279066624.0);
-        const double b = sm.table[kj & 255];
+        const double b = smp_shared().table[kj & 255];
         double q = fma(f, 0.009618129107628477, 0.05550410866482158);
         q = fma(f, q, 0.2402265069591007);
         q = fma(f, q, 0.6931471805599453);
-        double e = fma(b * f, q, b);
-        e = __hiloint2double(__double2hiint(e) + (((kj >> 8) + fix) << 20), __double2loint(e));
-        return e < min_w ? 0 : __double_as_longlong(e + 4503599627370496.0) & 0xfffffffffffffull;
+        const double e = fma(b * f, q, b);
+        const double g = __hiloint2double(__double2hiint(e) + ((kj & ~255) << 12), __double2loint(e));
+        return __double_as_longlong(g + 4503599627370496.0) & 0xfffffffffffffull;
     }
-    __device__ __forceinline__ bool kept(float l, int i) const {
-        return l > cut_val || (l == cut_val && index(i) <= cut_idx);
+    // f32 -> f64 with integer operations, as the conversion unit has an eighth of their rate: a
+    // zero or denormal value comes out up to 2^-126 off.
+    __device__ static __forceinline__ double widen(float x) {
+        const int b = __float_as_int(x);
+        return __hiloint2double(((b >> 3) & 0x8fffffff) + 0x38000000, b << 29);
     }
-    __device__ __forceinline__ bool in_range(float l, int i) const { return l >= vmin && l <= vmax && kept(l, i); }
-    __device__ __forceinline__ int bin_of(float l) const {
-        return linear ? min(SMP_BINS - 1, (int)(fmaf(-0.25f, l, vhi) * inv)) : (int)((smp_key(vmax) - smp_key(l)) >> shift);
-    }
-    // The slice's elements, four at a time per thread.
-    template <typename F>
-    __device__ __forceinline__ void each(F f) const {
-#pragma unroll 2
-        for (int i = 4 * threadIdx.x; i < n; i += 4 * SMP_THREADS) {
-            const float4 x = at4(i);
-            f(x.x, i);
-            f(x.y, i + 1);
-            f(x.z, i + 2);
-            f(x.w, i + 3);
+    // The weights of four elements together, so that their chains overlap; 0 below min_p and
+    // where not ok (-inf never is).  What lies below `lowest` has weight 0 and is raised to
+    // it.  A row whose T could tell widen's error, or is so small that nothing lies between the
+    // top and weight 0, goes the plain way (coarse).
+    __device__ __forceinline__ void weight4(const float (&l)[4], const bool (&ok)[4], u64 (&v)[4]) const {
+        double t[4];
+        if (!coarse) {  // uniform
+#pragma unroll
+            for (int e = 0; e < 4; e++) t[e] = (widen(fmaxf(l[e], lowest)) - topd) * scale;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                t[e] = ((double)l[e] - (double)top) * scale;
+                t[e] = t[e] > floor_t ? t[e] : floor_t;
+            }
         }
+#pragma unroll
+        for (int e = 0; e < 4; e++) v[e] = weight_of(t[e]);
+#pragma unroll
+        for (int e = 0; e < 4; e++) v[e] = ok[e] && v[e] >= min_w ? v[e] : 0;
+    }
+    __device__ __forceinline__ u64 weight1(float l) const {
+        const double t = coarse ? fmax(((double)l - (double)top) * scale, floor_t)
+                                : (widen(fmaxf(l, lowest)) - topd) * scale;
+        const u64 v = weight_of(t);
+        return v >= min_w ? v : 0;
+    }
+    // Above the cut; i counts from the slice's first element.
+    __device__ __forceinline__ bool kept(float l, int i) const { return l > cut_val || (l == cut_val && i <= cut_i); }
+    __device__ __forceinline__ bool in_range(float l, int i) const {
+        return (l > low_val || (l == low_val && i <= low_i)) && l <= vmax;
+    }
+    // (a value below 2^23 plus 2^23 holds the nearest whole number in its low bits)
+    __device__ __forceinline__ int bin_of(float l) const {
+        return linear ? min(SMP_BINS - 1, __float_as_int(fmaf(fmaf(-0.25f, l, vhi), inv, 8388608.0f)) - 0x4b000000)
+                      : (int)((smp_key(vmax) - smp_key(l)) >> shift);
+    }
+    // Moves the cut to the element of an order code.
+    __device__ __forceinline__ void cut_at(u64 code) {
+        cut_val = smp_value((uint32_t)(code >> 32));
+        const int64_t i = (int64_t)(uint32_t)~(uint32_t)code - first;
+        cut_i = i > INT_MAX ? INT_MAX : i < 0 ? -1 : (int)i;
     }
 
-    // Exchange of four words per CTA (thread 0's); after it every CTA holds all of them in
-    // the returned box.  Boxes alternate: a CTA may write the next exchange while another
-    // still reads this one.
+    // Exchange of four words per CTA (those of thread t < C, alike in all of them); after it
+    // every CTA holds all of them in the returned box.  Boxes alternate: a CTA may write the
+    // next exchange while another still reads this one.
     __device__ __forceinline__ const u64 (*exchange(u64 a, u64 b, u64 c, u64 d))[SMP_MAX_CLUSTER] {
-        u64(*box)[SMP_MAX_CLUSTER] = sm.box[phase++ & 1];
+        u64(*box)[SMP_MAX_CLUSTER] = smp_shared().box[phase++ & 1];
         if ((int)threadIdx.x < C) {
             u64* dst = cl.map_shared_rank(&box[0][0], threadIdx.x);
             dst[r] = a;
@@ -201,27 +258,41 @@ struct SampleRow {
     // sums before each coarse bin, starting from c0, m0.  by_value spreads the values evenly
     // over the bins (both sides scaled by 1/4, so that no difference overflows; monotone, as
     // each operation rounds monotonically); else the codes, which always splits the range.
-    __device__ void histogram(float lo, float hi, bool by_value, bool mass, u64 c0, u64 m0) {
+    __device__ __forceinline__ void histogram(float lo, float hi, bool by_value, bool clear, bool mass, u64 c0, u64 m0) {
+        SampleShared& sm = smp_shared();
         vmin = lo;
         vmax = hi;
+        low_val = fmaxf(lo, cut_val);
+        low_i = lo > cut_val ? INT_MAX : cut_i;
         vhi = 0.25f * hi;
         const float span = vhi - 0.25f * lo;
         inv = (float)SMP_BINS / span;
         shift = max(0, 32 - __clz(smp_key(hi) - smp_key(lo)) - 11);
         linear = by_value && span > 0.0f && inv < 1e30f;
-        for (int i = threadIdx.x; i < SMP_BINS; i += SMP_THREADS) sm.cnt[i] = sm.lo[i] = sm.hi[i] = 0;
-        __syncthreads();
-        each([&](float l, int i) {
-            if (!in_range(l, i)) return;
-            const int b = bin_of(l);
-            if (mass) {
-                const u64 wt = weight(l);
-                if (wt == 0) return;  // no candidate, or one that no mass limit can tell apart
-                const uint32_t wl = (uint32_t)wt, old = atomicAdd(&sm.lo[b], wl);
-                const uint32_t wh = (uint32_t)(wt >> 32) + (old + wl < old ? 1u : 0u);
-                if (wh) atomicAdd(&sm.hi[b], wh);
+        if (clear) {
+            for (int i = threadIdx.x; i < SMP_BINS; i += SMP_THREADS) sm.cnt[i] = sm.lo[i] = sm.hi[i] = 0;
+            __syncthreads();
+        }
+        each(0, n, threadIdx.x, SMP_THREADS, [&](const float4& x, int i) {
+            const float l[4] = {x.x, x.y, x.z, x.w};
+            bool ok[4];
+#pragma unroll
+            for (int e = 0; e < 4; e++) ok[e] = in_range(l[e], i + e);
+            if (!(ok[0] | ok[1] | ok[2] | ok[3])) return;
+            u64 v[4];
+            if (mass) weight4(l, ok, v);
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                // a weight of 0: no candidate, or one that no mass limit can tell apart
+                if (!ok[e] || (mass && v[e] == 0)) continue;
+                const int b = bin_of(l[e]);
+                if (mass) {  // two 32-bit adds: a 64-bit one is a compare-and-swap loop
+                    const uint32_t wl = (uint32_t)v[e], old = atomicAdd(&sm.lo[b], wl);
+                    const uint32_t wh = (uint32_t)(v[e] >> 32) + (old + wl < old ? 1u : 0u);
+                    if (wh) atomicAdd(&sm.hi[b], wh);
+                }
+                atomicAdd(&sm.cnt[b], 1u);
             }
-            atomicAdd(&sm.cnt[b], 1u);
         });
         __syncthreads();
         for (int cb = w; cb < SMP_COARSE; cb += SMP_WARPS) {
@@ -257,228 +328,49 @@ struct SampleRow {
         __syncthreads();
     }
 
-    // The cut at the first `limit` candidates (by_count), or at the candidates whose preceding
-    // mass is < limit; the present histogram holds the border.  Its bins are lost (false) where
-    // the crossing one had to be spread again.  mass: the histogram has masses.
-    __device__ bool narrow(bool by_count, bool mass, u64 limit) {
-        bool whole = true;
-        for (;;) {
-            // the crossing bin: the first with count (mass) up to its end >= limit
-            if (w == 0) {
-                const u64* before = by_count ? sm.before_c : sm.before_m;
-                const bool x0 = before[lane] < limit && before[lane + 1] >= limit;
-                const bool x1 = before[lane + 32] < limit && before[lane + 33] >= limit;
-                const uint32_t y0 = __ballot_sync(0xffffffffu, x0), y1 = __ballot_sync(0xffffffffu, x1);
-                const int cb = y0 ? __ffs(y0) - 1 : 31 + __ffs(y1);
-                const int b = 32 * cb + lane;
-                u64 c = 0, m = 0;
+    // The crossing bin of the present histogram, the first with count (mass) up to its end
+    // >= limit: into sm.found.  Warp 0 of every CTA.
+    __device__ __forceinline__ void cross(bool by_count, u64 limit) {
+        SampleShared& sm = smp_shared();
+        const u64* before = by_count ? sm.before_c : sm.before_m;
+        const bool x0 = before[lane] < limit && before[lane + 1] >= limit;
+        const bool x1 = before[lane + 32] < limit && before[lane + 33] >= limit;
+        const uint32_t y0 = __ballot_sync(0xffffffffu, x0), y1 = __ballot_sync(0xffffffffu, x1);
+        const int cb = y0 ? __ffs(y0) - 1 : 31 + __ffs(y1);
+        const int b = 32 * cb + lane;
+        u64 c = 0, m = 0;
 #pragma unroll 8
-                for (int t = 0; t < C; t++) {
-                    const SampleShared* o = cl.map_shared_rank(&sm, t);
-                    c += o->cnt[b];
-                    m += ((u64)o->hi[b] << 32) + o->lo[b];
-                }
-                const u64 ec = sm.before_c[cb] + smp_warp_scan(c, lane) - c, em = sm.before_m[cb] + smp_warp_scan(m, lane) - m;
-                const u64 x = by_count ? ec : em, y = x + (by_count ? c : m);
-                if (x < limit && y >= limit) {
-                    sm.found_bin = b;
-                    sm.found[0] = ec;
-                    sm.found[1] = em;
-                    sm.found[2] = c;
-                }
-                if (lane == 0) sm.best = 0;
-            }
-            if (r == 0 && threadIdx.x == 32) sm.n_list = 0;
-            // CTA 0's counter is zero, and every CTA has read the bins, before any goes on
-            cl.sync();
-            const int bin = (int)sm.found_bin;
-            const u64 c0 = sm.found[0], m0 = sm.found[1];
-            // What lies below this is behind the bin: its lower edge, less a hundredth of a bin
-            // for the rounding of bin_of and a few units in the last place for its own.
-            const float under = linear ? 4.0f * (vhi - ((float)bin + 1.01f) / inv) - 4e-6f * fabsf(vhi) : vmin;
-            if (sm.found[2] <= SMP_LIST) {
-                each([&](float l, int i) {
-                    if (l < under || !in_range(l, i) || bin_of(l) != bin) return;
-                    const u64 wt = mass ? weight(l) : 0;
-                    if (mass && wt == 0) return;
-                    const uint32_t slot = atomicAdd(cl.map_shared_rank(&sm.n_list, 0), 1u);
-                    if (slot >= SMP_LIST) return;
-                    const u64 code = ((u64)smp_key(l) << 32) | (uint32_t)~index(i);
-                    for (int t = 0; t < C; t++) {
-                        SampleShared* o = cl.map_shared_rank(&sm, t);
-                        o->lcode[slot] = code;
-                        o->lw[slot] = wt;
-                    }
-                });
-                cl.sync();
-                // each gathered element's rank: the last one kept is the cut
-                const int m = (int)sm.found[2], e = (int)threadIdx.x;
-                const u64 code = e < m ? sm.lcode[e] : 0;
-                uint32_t rank = 0;
-                u64 pre = m0;
-                bool in = false;
-                if (e < m) {
-#pragma unroll 4
-                    for (int j = 0; j < m; j++) {
-                        const bool is_before = sm.lcode[j] > code;
-                        rank += is_before;
-                        pre += is_before ? sm.lw[j] : 0;
-                    }
-                    in = (by_count ? c0 + rank : pre) < limit;
-                }
-                const uint32_t last = __reduce_max_sync(0xffffffffu, in ? rank + 1 : 0);
-                if (lane == 0 && last) atomicMax(&sm.best, last);
-                __syncthreads();
-                if (in && rank + 1 == sm.best) sm.cut = code, sm.kept_mass = pre + sm.lw[e];
-                __syncthreads();
-                break;
-            }
-            // too many to rank: the bin's own range of codes
-            whole = false;
-            uint32_t a = 0, b = 0;  // largest code, largest complement
-            if (linear) {
-                each([&](float l, int i) {
-                    if (l < under || !in_range(l, i) || bin_of(l) != bin) return;
-                    a = max(a, smp_key(l));
-                    b = max(b, ~smp_key(l));
-                });
-                a = __reduce_max_sync(0xffffffffu, a);
-                b = __reduce_max_sync(0xffffffffu, b);
-                if (lane == 0) sm.red[0][w] = a, sm.red[1][w] = b;
-                __syncthreads();
-                for (int j = 0; j < SMP_WARPS; j++) a = max(a, (uint32_t)sm.red[0][j]), b = max(b, (uint32_t)sm.red[1][j]);
-                const u64(*box)[SMP_MAX_CLUSTER] = exchange(a, b, 0, 0);
-                for (int t = 0; t < C; t++) a = max(a, (uint32_t)box[0][t]), b = max(b, (uint32_t)box[1][t]);
-                b = ~b;
-            } else {
-                a = smp_key(vmax) - ((uint32_t)bin << shift);
-                b = max(smp_key(vmin), shift ? a - ((1u << shift) - 1u) : a);
-            }
-            if (a != b) {
-                histogram(smp_value(b), smp_value(a), false, mass, c0, m0);
-                continue;
-            }
-            // all equal: the first q of them in index order
-            const float tie = smp_value(a);
-            const u64 wt = mass ? weight(tie) : 0;
-            const u64 q = by_count ? limit - c0 : (limit - m0 + wt - 1) / wt;  // before = m0 + j wt < limit
-            locate([&](float l, int i) -> u64 { return l == tie && kept(l, i) ? 1 : 0; }, tie, q - 1, -1.0, 0.0, 0.0, 0.0,
-                   [&](float, uint32_t at) {
-                       for (int t = 0; t < C; t++) *cl.map_shared_rank(&sm.cut, t) = ((u64)a << 32) | (uint32_t)~at;
-                   });
-            if (threadIdx.x == 0) sm.kept_mass = m0 + q * wt;
-            cl.sync();
-            break;
-        }
-        cut_val = smp_value((uint32_t)(sm.cut >> 32));
-        cut_idx = ~(uint32_t)sm.cut;
-        return whole;
-    }
-
-    // The first element, in index order, whose running sum of weight_of exceeds `target`
-    // (below the row's total); with u >= 0 the target is min(floor(u * total), total - 1).
-    // Elements below `under` weigh nothing.  Calls hit(value, index) on the one thread that
-    // finds it.  s1, s2, s3: this warp's sums, which the same exchange adds up over the row
-    // (into sums[]).
-    template <typename W, typename H>
-    __device__ void locate(W weight_of, float under, u64 target, double u, double s1, double s2, double s3, H hit) {
-        const int per = ((n + SMP_WARPS - 1) / SMP_WARPS + 3) & ~3;  // a warp's contiguous share
-        const int lo = min(n, w * per), hi = min(n, lo + per);
-        u64 s = 0;
-        auto four = [&](const float4& x, int i, u64 (&v)[4]) {
-            v[0] = x.x >= under ? weight_of(x.x, i) : 0;
-            v[1] = x.y >= under ? weight_of(x.y, i + 1) : 0;
-            v[2] = x.z >= under ? weight_of(x.z, i + 2) : 0;
-            v[3] = x.w >= under ? weight_of(x.w, i + 3) : 0;
-        };
-#pragma unroll 2
-        for (int i = lo + 4 * lane; i < hi; i += 128) {
-            u64 v[4];
-            four(at4(i), i, v);
-            s += (v[0] + v[1]) + (v[2] + v[3]);
-        }
-        s = smp_warp_sum(s);
-        __syncthreads();
-        if (lane == 0) {
-            sm.red[0][w] = s;
-            sm.red[1][w] = __double_as_longlong(s1);
-            sm.red[2][w] = __double_as_longlong(s2);
-            sm.red[3][w] = __double_as_longlong(s3);
-        }
-        __syncthreads();
-        u64 mine = 0;
-        s1 = s2 = s3 = 0.0;
-        for (int j = 0; j < SMP_WARPS; j++) {
-            mine += sm.red[0][j];
-            s1 += __longlong_as_double(sm.red[1][j]);
-            s2 += __longlong_as_double(sm.red[2][j]);
-            s3 += __longlong_as_double(sm.red[3][j]);
-        }
-        const u64(*box)[SMP_MAX_CLUSTER] =
-            exchange(mine, __double_as_longlong(s1), __double_as_longlong(s2), __double_as_longlong(s3));
-        u64 before = 0, total = 0;
-        s1 = s2 = s3 = 0.0;
         for (int t = 0; t < C; t++) {
-            if (t < r) before += box[0][t];
-            total += box[0][t];
-            s1 += __longlong_as_double(box[1][t]);
-            s2 += __longlong_as_double(box[2][t]);
-            s3 += __longlong_as_double(box[3][t]);
+            const SampleShared* o = cl.map_shared_rank(&sm, t);
+            c += o->cnt[b];
+            m += ((u64)o->hi[b] << 32) + o->lo[b];
         }
-        sums[0] = s1;
-        sums[1] = s2;
-        sums[2] = s3;
-        if (u >= 0.0) {
-            target = (u64)(u * (double)total);
-            if (target >= total) target = total - 1;
-        }
-        if (target < before || target - before >= mine) return;  // another CTA's (uniform)
-        u64 run = before;
-        int wi = 0;
-        while (run + sm.red[0][wi] <= target) run += sm.red[0][wi++];
-        const int a = min(n, wi * per), b = min(n, a + per);
-        for (int i0 = a; i0 < b; i0 += 4 * SMP_THREADS) {
-            const int i = i0 + 4 * (int)threadIdx.x;
-            u64 v[4] = {0, 0, 0, 0};
-            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (i < b) {
-                x = at4(i);
-                four(x, i, v);
-            }
-            const u64 sum = (v[0] + v[1]) + (v[2] + v[3]);
-            const u64 inc = smp_warp_scan(sum, lane);
-            __syncthreads();
-            if (lane == 31) sm.red[1][w] = inc;
-            __syncthreads();
-            u64 upto = run + inc - sum;
-            for (int j = 0; j < SMP_WARPS; j++) {
-                const u64 y = sm.red[1][j];
-                upto += j < w ? y : 0;
-                run += y;
-            }
-            const float xs[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-                if (v[e] != 0 && upto <= target && upto + v[e] > target) hit(xs[e], index(i + e));
-                upto += v[e];
-            }
+        const u64 ec = sm.before_c[cb] + smp_warp_scan(c, lane) - c, em = sm.before_m[cb] + smp_warp_scan(m, lane) - m;
+        const u64 x = by_count ? ec : em, y = x + (by_count ? c : m);
+        if (x < limit && y >= limit) {
+            sm.found_bin = b;
+            sm.found_upto = (uint32_t)min(ec + c, (u64)0xffffffffu);
+            sm.found[0] = ec;
+            sm.found[1] = em;
         }
     }
-    double sums[3];
 };
 
 // Grid (C * rows), clusters of C.
 __global__ void __launch_bounds__(SMP_THREADS, 2) sample_kernel(const __grid_constant__ SampleArgs a) {
-    extern __shared__ __align__(1024) uint8_t smem[];
-    SampleShared& sm = *reinterpret_cast<SampleShared*>(smem);
-    SampleRow row{cooperative_groups::this_cluster(), sm};
-    const int C = row.C = (int)row.cl.num_blocks(), r = row.r = (int)row.cl.block_rank();
+    SampleShared& sm = smp_shared();
+    SampleRow row{cooperative_groups::this_cluster()};
+    cooperative_groups::cluster_group& cl = row.cl;
+    const int C = row.C = (int)cl.num_blocks(), r = row.r = (int)cl.block_rank();
     const int64_t i_row = blockIdx.x / C;
-    row.w = threadIdx.x >> 5;
-    row.lane = threadIdx.x & 31;
+    const int w = row.w = threadIdx.x >> 5, lane = row.lane = threadIdx.x & 31;
     row.phase = 0;
-    row.cl.barrier_arrive();  // every CTA has started before another writes into it (waited for below)
-    if (threadIdx.x < SMP_TABLE) sm.table[threadIdx.x] = exp2((double)threadIdx.x / SMP_TABLE);
+    cl.barrier_arrive();  // every CTA has started before another writes into it (waited for below)
+    if (threadIdx.x == 0) {
+        mbar_init(&sm.landed, 1);
+        fence_mbar_init();
+        sm.n_list = 0;
+    }
     pdl_trigger();
     pdl_wait();
 
@@ -486,28 +378,59 @@ __global__ void __launch_bounds__(SMP_THREADS, 2) sample_kernel(const __grid_con
     // first one begins up to three elements before the row.
     row.src = a.logits + i_row * a.ldl;
     row.V = a.V;
-    row.cache = reinterpret_cast<float*>(smem + sizeof(SampleShared));
-    const int64_t before = (int64_t)(reinterpret_cast<uintptr_t>(row.src) >> 2 & 3);
-    row.first = (int64_t)r * a.slice - before;
+    row.first = (int64_t)r * a.slice - (int64_t)(reinterpret_cast<uintptr_t>(row.src) >> 2 & 3);
     const int64_t left = a.V - row.first;
     const int n = row.n = (int)(left < a.slice ? max((int64_t)0, (left + 3) & ~(int64_t)3) : a.slice);
     row.cached = min(n, a.cached);
 
     const float T = a.temperature ? __ldg(a.temperature + i_row) : 1.0f;
     const bool greedy = !(T > 0.0f);
+    const double Td = greedy ? 1.0 : (double)T;
     const float mp = a.min_p ? __ldg(a.min_p + i_row) : 0.0f;
+    const double min_p = mp > 0.0f ? fmin((double)mp, 1.0) : 0.0;
     const float p = a.top_p ? __ldg(a.top_p + i_row) : 1.0f;
     const int32_t k = greedy ? 1 : a.top_k ? __ldg(a.top_k + i_row) : 0;
     float u = a.u ? __ldg(a.u + i_row) : 0.0f;
     u = u > 0.0f ? fminf(u, 1.0f) : 0.0f;  // NaN counts as 0
 
-    // the slice into shared memory; the row's largest and smallest finite logit
+    // The slice into shared memory: what the row fills of its 16-byte vectors by bulk copies of
+    // eight lanes, the vectors at the row's ends by two threads; meanwhile the table, the
+    // cleared histogram and what depends on the row's parameters.
+    if (w == 0) {
+        const int i0 = row.first < 0 ? 4 : 0;
+        const int i1 = max(i0, min(row.cached, (int)min((int64_t)n, left & ~(int64_t)3)));
+        const int part = ((i1 - i0) / 8 + 3) & ~3;
+        const int from = min(i1, i0 + lane * part), to = lane == 7 ? i1 : min(i1, from + part);
+        if (lane == 0) mbar_arrive_expect_tx(&sm.landed, (uint32_t)(i1 - i0) * 4);
+        __syncwarp();
+        if (lane < 8 && to > from)
+            bulk_g2s_hint(smp_cache() + from, row.src + row.first + from, (uint32_t)(to - from) * 4, &sm.landed,
+                          policy_evict_first());
+        const int edge = lane == 8 && i0 > 0 ? 0 : lane == 9 && i1 < row.cached && i1 >= i0 ? i1 : -1;
+        if (edge >= 0 && edge < row.cached) *reinterpret_cast<float4*>(smp_cache() + edge) = row.load4(edge);
+    } else if (w == 1 && lane == 0) {
+        sm.scale = 1.4426950408889634 / Td;
+        sm.ln_min_p = min_p > 0.0 ? log(min_p) : 0.0;
+    }
+    if (threadIdx.x >= SMP_THREADS - SMP_TABLE) {
+        const int i = threadIdx.x - (SMP_THREADS - SMP_TABLE);
+        sm.table[i] = exp2((double)i / SMP_TABLE + a.fix);
+    }
+    for (int i = threadIdx.x; i < SMP_BINS; i += SMP_THREADS) sm.cnt[i] = sm.lo[i] = sm.hi[i] = 0;
+    __syncthreads();  // the barrier and the edges are there
+    {
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(&sm.landed, 0))
+            if (globaltimer_ns() - t0 > 2000000000ull) {
+                set_err(ERR_TIMEOUT);
+                break;
+            }
+    }
+
+    // the row's largest and smallest finite logit
     float hi = -INFINITY, lo = INFINITY;
     bool bad = false;
-#pragma unroll 4
-    for (int i = 4 * threadIdx.x; i < n; i += 4 * SMP_THREADS) {
-        const float4 x = row.load4(i);
-        if (i < row.cached) *reinterpret_cast<float4*>(row.cache + i) = x;
+    row.each(0, n, threadIdx.x, SMP_THREADS, [&](const float4& x, int) {
         const float xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int e = 0; e < 4; e++) {
@@ -515,18 +438,19 @@ __global__ void __launch_bounds__(SMP_THREADS, 2) sample_kernel(const __grid_con
             hi = fmaxf(hi, xs[e]);
             lo = fminf(lo, xs[e] > -INFINITY ? xs[e] : INFINITY);
         }
-    }
+    });
     uint32_t m1 = __reduce_max_sync(0xffffffffu, smp_key(hi)), m2 = __reduce_max_sync(0xffffffffu, ~smp_key(lo));
     uint32_t m3 = __any_sync(0xffffffffu, bad);
-    if (row.lane == 0) sm.red[0][row.w] = m1, sm.red[1][row.w] = m2, sm.red[2][row.w] = m3;
+    if (lane == 0) sm.red[0][w] = m1, sm.red[1][w] = m2, sm.red[2][w] = m3;
     __syncthreads();
-    for (int j = 0; j < SMP_WARPS; j++)
-        m1 = max(m1, (uint32_t)sm.red[0][j]), m2 = max(m2, (uint32_t)sm.red[1][j]), m3 |= (uint32_t)sm.red[2][j];
-    row.cl.barrier_wait();
+    auto max_of = [&](const u64* v, int count) {
+        return __reduce_max_sync(0xffffffffu, lane < count ? (uint32_t)v[lane] : 0u);
+    };
+    if (w == 0) m1 = max_of(sm.red[0], SMP_WARPS), m2 = max_of(sm.red[1], SMP_WARPS), m3 = max_of(sm.red[2], SMP_WARPS);
+    cl.barrier_wait();
     {
         const u64(*box)[SMP_MAX_CLUSTER] = row.exchange(m1, m2, m3, 0);
-        for (int t = 0; t < C; t++)
-            m1 = max(m1, (uint32_t)box[0][t]), m2 = max(m2, (uint32_t)box[1][t]), m3 |= (uint32_t)box[2][t];
+        m1 = max_of(box[0], C), m2 = max_of(box[1], C), m3 = max_of(box[2], C);
     }
     const float top = row.top = smp_value(m1), bottom = smp_value(~m2);
     if (m3 || top == -INFINITY) {  // uniform over the cluster
@@ -538,14 +462,16 @@ __global__ void __launch_bounds__(SMP_THREADS, 2) sample_kernel(const __grid_con
         }
         return;
     }
-    const double Td = greedy ? 1.0 : (double)T;
-    const double min_p = mp > 0.0f ? fmin((double)mp, 1.0) : 0.0;
-    row.scale = 1.4426950408889634 / Td;
-    row.fix = a.fix;
-    row.least = -(double)(a.fix + 2);
-    row.min_w = min_p * (double)(1ull << a.fix);
-    row.cut_val = -INFINITY;
-    row.cut_idx = 0xffffffffu;
+    row.scale = sm.scale;
+    row.min_w = __double2ull_rn(min_p * (double)(1ull << a.fix));
+    row.floor_t = -(double)(a.fix + 2);
+    // 2^-(fix + 1.5) of the top, rounded down (and by a hair more than its own rounding)
+    const double deep = (a.fix + 1.5) * 0.6931471805599453, hair = fabs((double)top) * 1e-12;
+    row.lowest = fmaxf(-FLT_MAX, __double2float_rd((double)top - deep * 1.000001 * Td - hair));
+    row.coarse = Td < 1e-18 || ((double)top - (double)row.lowest) * row.scale > 1000.0;
+    row.topd = SampleRow::widen(top);
+    row.cut_val = bottom;  // everything finite
+    row.cut_i = INT_MAX;
 
     // plain softmax: mass and first moment of the elements below the largest, and the
     // number equal to it (kept apart, so that a peaked row's small entropy stays exact)
@@ -553,54 +479,340 @@ __global__ void __launch_bounds__(SMP_THREADS, 2) sample_kernel(const __grid_con
     if (a.conf || a.entropy) {
         float e1 = 0.0f, e2 = 0.0f;
         uint32_t eq = 0;
-        row.each([&](float l, int) {
-            const float z = fmaxf(l - top, -200.0f);  // e^-200 is 0 in f32
-            const float e = z < 0.0f ? exp2f(z * 1.4426950408889634f) : 0.0f;
-            eq += z == 0.0f;
-            e1 += e;
-            e2 = fmaf(e, z, e2);
+        row.each(0, n, threadIdx.x, SMP_THREADS, [&](const float4& x, int) {
+            const float l[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const float z = fmaxf(l[j] - top, -200.0f);  // e^-200 is 0 in f32
+                const float e = z < 0.0f ? exp2f(z * 1.4426950408889634f) : 0.0f;
+                eq += z == 0.0f;
+                e1 += e;
+                e2 = fmaf(e, z, e2);
+            }
         });
         s1 = smp_warp_sum((double)e1);
         s2 = smp_warp_sum((double)e2);
         s3 = (double)__reduce_add_sync(0xffffffffu, eq);
     }
 
-    // Limits.  min_p is part of the weight; a count limit needs masses only where a mass
-    // limit follows it.
-    const bool by_p = !(p >= 1.0f) && k != 1;
-    const bool mass = by_p || min_p > 0.0;
-    if (k > 0 || by_p) {
-        // The bins need not reach below the values whose weight is 0 (with some room for the
-        // rounding of either side).
-        float floor_v = bottom;
-        if (mass) {
-            const double deep = fmin(-row.least * 0.6931471805599453, min_p > 0.0 ? -log(min_p) : INFINITY);
-            floor_v = fmaxf(bottom, __double2float_rd((double)top - (deep * 1.000001 + 1e-12) * Td - fabs((double)top) * 1e-12));
+    // Every CTA has all of them after the next cluster barrier.
+    {
+        if (lane == 0) {
+            sm.red[1][w] = __double_as_longlong(s1);
+            sm.red[2][w] = __double_as_longlong(s2);
+            sm.red[3][w] = __double_as_longlong(s3);
         }
-        row.histogram(floor_v, top, true, mass, 0, 0);
-        u64 total = sm.before_m[SMP_COARSE];
-        bool whole = true;
-        if (k > 0 && (u64)k < sm.before_c[SMP_COARSE]) {
-            whole = row.narrow(true, mass, (u64)k);
-            total = sm.kept_mass;
-        }
-        if (by_p) {
-            if (!whole) row.histogram(fmaxf(floor_v, row.cut_val), top, true, mass, 0, 0);
-            // preceding mass < p S of whole numbers: preceding mass < ceil(p S); at least 1
-            // keeps the first candidate
-            const u64 limit = (u64)ceil((p > 0.0f ? (double)p : 0.0) * (double)total);
-            row.narrow(false, mass, limit < 1 ? 1 : limit);
+        __syncthreads();
+        if (w < 3) {
+            const u64 sum =
+                __double_as_longlong(smp_warp_sum(lane < SMP_WARPS ? __longlong_as_double(sm.red[1 + w][lane]) : 0.0));
+            if (lane < C) *cl.map_shared_rank(&sm.plain[w][r], lane) = sum;
         }
     }
+    auto plain_sum = [&](int which) {
+        double x = 0.0;
+        for (int t = 0; t < C; t++) x += __longlong_as_double(sm.plain[which][t]);
+        return x;
+    };
+    // The token (one thread of the row), and the row's entropy with it.
+    auto report = [&](float l, uint32_t at) {
+        const double below = plain_sum(0), others = plain_sum(2) - 1.0, all = (1.0 + others) + below;
+        a.token[i_row] = (int32_t)at;
+        if (a.conf) a.conf[i_row] = (float)(exp((double)l - (double)top) / all);
+        if (a.entropy) a.entropy[i_row] = (float)(log1p(others + below) - plain_sum(1) / all);
+    };
 
-    // After this exchange no CTA reads or writes another's memory: they leave one by one.
-    row.locate([&](float l, int i) -> u64 { return row.kept(l, i) ? row.weight(l) : 0; }, row.cut_val, 0, (double)u, s1, s2,
-               s3, [&](float l, uint32_t at) {
-                   a.token[i_row] = (int32_t)at;
-                   if (a.conf) a.conf[i_row] = (float)(exp((double)l - (double)top) / (row.sums[0] + row.sums[2]));
-               });
-    if (a.entropy && r == 0 && threadIdx.x == 0)
-        a.entropy[i_row] = (float)(log1p(row.sums[0] + (row.sums[2] - 1.0)) - row.sums[1] / (row.sums[0] + row.sums[2]));
+    // Stage 0: top_k; stage 1: top_p; stage 2: the token.  min_p is part of the weight; a count
+    // limit needs masses only where min_p or a mass limit follows it, or the list below ends it.
+    const bool by_p = !(p >= 1.0f) && k != 1;
+    const bool mass = by_p || min_p > 0.0;
+    bool have = false, clear = false;  // the histogram over all candidates is there; must be cleared first
+    bool cut_mass = false;
+    int half = 0;       // which list comes next
+#pragma unroll 1
+    for (int stage = 0; stage < 3; stage++) {
+        const bool by_count = stage == 0;
+        bool tie = false;
+        float tie_val = 0.0f;
+        u64 target = 0, tie_mass = 0;
+        if (stage < 2) {
+            if (!(by_count ? k > 0 : by_p)) continue;
+            float from = fmaxf(bottom, row.cut_val), to = top;
+            if (mass) {
+                // no bins for values whose weight is 0 (with some room for either side's rounding)
+                from = fmaxf(from, row.lowest);
+                if (min_p > 0.0)
+                    from = fmaxf(from, __double2float_rd((double)top - (-sm.ln_min_p * 1.000001 + 1e-12) * Td - hair));
+            }
+            u64 c0 = 0, m0 = 0, limit = 0;
+            bool whole = true, done = false;
+#pragma unroll 1
+            while (!done) {
+                if (!have) row.histogram(from, to, whole, clear, mass, c0, m0);
+                have = clear = true;
+                int bin = SMP_BINS - 1;
+                uint32_t upto = 0;
+                bool all = false;  // no limit is reached
+                if (whole) {
+                    const u64 candidates = sm.before_c[SMP_COARSE];
+                    if (by_count) {
+                        limit = (u64)k;
+                        all = limit >= candidates;
+                    } else {
+                        // preceding mass < p S of whole numbers: preceding mass < ceil(p S); at
+                        // least 1 keeps the first candidate
+                        const u64 S = cut_mass ? sm.kept_mass : sm.before_m[SMP_COARSE];
+                        limit = (u64)ceil((p > 0.0f ? (double)p : 0.0) * (double)S);
+                        if (limit < 1) limit = 1;
+                    }
+                    upto = (uint32_t)min(candidates, (u64)0xffffffffu);
+                    if (all && upto > SMP_LIST) break;
+                }
+                if (!all) {
+                    if (w == 0) {
+                        row.cross(by_count, limit);
+                        if (lane == 0) sm.best = 0, sm.n_mine[half] = 0;
+                    }
+                    __syncthreads();
+                    bin = (int)sm.found_bin;
+                    upto = sm.found_upto;
+                    c0 = sm.found[0];
+                    m0 = sm.found[1];
+                }
+                if (whole && upto <= SMP_LIST) {
+                    // Few candidates up to the end of the crossing bin (any cut of an earlier
+                    // stage included): CTA 0 ranks them all and takes the token from them.
+                    row.each(0, n, threadIdx.x, SMP_THREADS, [&](const float4& x, int i) {
+                        const float l[4] = {x.x, x.y, x.z, x.w};
+                        if (!(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])) >= row.low_val)) return;
+#pragma unroll
+                        for (int e = 0; e < 4; e++)
+                            if (row.in_range(l[e], i + e) && row.kept(l[e], i + e) && row.bin_of(l[e]) <= bin) {
+                                if (mass && row.weight1(l[e]) == 0) continue;
+                                SampleShared* o = cl.map_shared_rank(&sm, 0);
+                                const uint32_t slot = atomicAdd(&o->n_list, 1u);
+                                if (slot < SMP_LIST)
+                                    o->lcode[slot] = ((u64)smp_key(l[e]) << 32) | (uint32_t)~row.index(i + e);
+                            }
+                    });
+                    cl.sync();
+                    if (r != 0) return;  // nothing of this CTA's memory is read from here on
+                    const int m = (int)min(sm.n_list, (uint32_t)SMP_LIST), e = (int)threadIdx.x;
+                    const u64 code = e < m ? sm.lcode[e] : 0;
+                    const float l = smp_value((uint32_t)(code >> 32));
+                    u64 weight = e < m ? row.weight1(l) : 0;
+                    if (e < m) sm.lw[e] = weight;
+                    __syncthreads();
+                    uint32_t rank = 0;
+                    u64 pre = 0;
+                    if (e < m) {
+#pragma unroll 4
+                        for (int j = 0; j < m; j++) {
+                            const u64 other = sm.lcode[j], y = sm.lw[j];
+                            rank += other > code;
+                            pre += other > code ? y : 0;
+                        }
+                    }
+                    auto block_sum = [&](u64 y) {
+                        y = smp_warp_sum(y);
+                        __syncthreads();
+                        if (lane == 0) sm.red[0][w] = y;
+                        __syncthreads();
+                        return smp_warp_sum(lane < SMP_WARPS ? sm.red[0][lane] : 0ull);
+                    };
+                    bool in = e < m && (!by_count || rank < (uint32_t)k);
+                    if (by_count && by_p) {
+                        const u64 S = block_sum(in ? weight : 0);
+                        limit = (u64)ceil((p > 0.0f ? (double)p : 0.0) * (double)S);
+                        if (limit < 1) limit = 1;
+                    }
+                    in = in && (!by_p || pre < limit);
+                    if (!in) weight = 0;
+                    __syncthreads();
+                    if (e < m) sm.lw[e] = weight;
+                    const u64 total = block_sum(weight);
+                    target = (u64)((double)u * (double)total);
+                    if (target >= total) target = total - 1;
+                    if (in) {
+                        u64 run = 0;
+                        const uint32_t at = (uint32_t)code;  // complement of the index
+#pragma unroll 4
+                        for (int j = 0; j < m; j++) {
+                            const u64 y = sm.lw[j];
+                            run += (uint32_t)sm.lcode[j] > at ? y : 0;
+                        }
+                        if (run <= target && target - run < weight) report(l, ~at);
+                    }
+                    return;
+                }
+                // The bin's edges, with a hundredth of a bin for the rounding of bin_of and a
+                // few units in the last place for their own; the last bin reaches down.
+                const float slack = 4e-6f * fabsf(row.vhi);
+                const float under = !row.linear               ? row.vmin
+                                    : bin == SMP_BINS - 1 ? -INFINITY
+                                                          : 4.0f * (row.vhi - ((float)bin + 0.51f) / row.inv) - slack;
+                const float over = row.linear ? 4.0f * (row.vhi - ((float)bin - 0.51f) / row.inv) + slack : row.vmax;
+                uint32_t k_hi = 0, k_lo = 0;  // largest code of the bin, largest complement
+                row.each(0, n, threadIdx.x, SMP_THREADS, [&](const float4& x, int i) {
+                    const float l[4] = {x.x, x.y, x.z, x.w};
+                    bool ok[4];
+#pragma unroll
+                    for (int e = 0; e < 4; e++) ok[e] = l[e] <= over && l[e] >= under;
+                    if (!(ok[0] | ok[1] | ok[2] | ok[3])) return;
+#pragma unroll
+                    for (int e = 0; e < 4; e++)
+                        if (ok[e] && row.in_range(l[e], i + e) && row.bin_of(l[e]) == bin) {
+                            const uint32_t key = smp_key(l[e]), slot = atomicAdd(&sm.n_mine[half], 1u);
+                            k_hi = max(k_hi, key);
+                            k_lo = max(k_lo, ~key);
+                            if (slot < SMP_LIST) sm.mine[half][slot] = ((u64)key << 32) | (uint32_t)~row.index(i + e);
+                        }
+                });
+                cl.sync();  // also: every CTA has read the bins
+                const int n_of = lane < C ? (int)*cl.map_shared_rank(&sm.n_mine[half], lane) : 0;
+                const int e = (int)threadIdx.x;
+                int m = 0, source = 0, slot = 0;
+#pragma unroll 1
+                for (int t = 0; t < C; t++) {
+                    const int c = __shfl_sync(0xffffffffu, n_of, t);
+                    if (e >= m && e < m + c) source = t, slot = e - m;
+                    m += c;
+                }
+                done = m <= SMP_LIST;
+                if (done) {
+                    // each gathered element's rank: the last one kept is the cut
+                    u64 code = 0;
+                    if ((int)threadIdx.x < m) {
+                        code = cl.map_shared_rank(&sm, source)->mine[half][slot];
+                        sm.lcode[e] = code;
+                        sm.lw[e] = mass ? row.weight1(smp_value((uint32_t)(code >> 32))) : 0;
+                    }
+                    __syncthreads();
+                    uint32_t rank = 0;
+                    u64 pre = m0;
+                    bool in = false;
+                    if ((int)threadIdx.x < m) {
+#pragma unroll 4
+                        for (int j = 0; j < m; j++) {
+                            const u64 other = sm.lcode[j], weight = sm.lw[j];
+                            rank += other > code;
+                            pre += other > code ? weight : 0;
+                        }
+                        // what weighs nothing is no candidate where masses count
+                        in = (by_count ? c0 + rank : pre) < limit && (!mass || sm.lw[e] != 0);
+                    }
+                    const uint32_t last = __reduce_max_sync(0xffffffffu, in ? rank + 1 : 0);
+                    if (lane == 0 && last) atomicMax(&sm.best, last);
+                    __syncthreads();
+                    if (in && rank + 1 == sm.best) sm.cut = code, sm.kept_mass = pre + sm.lw[e];
+                    __syncthreads();
+                    row.cut_at(sm.cut);
+                    cut_mass = true;
+                } else {
+                    // too many to rank: the range of codes the bin really spans, or its ties
+                    k_hi = __reduce_max_sync(0xffffffffu, k_hi);
+                    k_lo = __reduce_max_sync(0xffffffffu, k_lo);
+                    if (lane == 0) sm.red[0][w] = k_hi, sm.red[1][w] = k_lo;
+                    __syncthreads();
+                    if (w == 0) k_hi = max_of(sm.red[0], SMP_WARPS), k_lo = max_of(sm.red[1], SMP_WARPS);
+                    const u64(*box)[SMP_MAX_CLUSTER] = row.exchange(k_hi, k_lo, 0, 0);
+                    k_hi = max_of(box[0], C), k_lo = ~max_of(box[1], C);
+                    from = smp_value(k_lo);
+                    to = smp_value(k_hi);
+                    whole = have = false;
+                    if (k_hi == k_lo) {  // all equal: the first ones in index order
+                        const u64 wt = mass ? row.weight1(to) : 0;
+                        target = by_count ? limit - c0 : (limit - m0 + wt - 1) / wt;  // before = m0 + j wt < limit
+                        tie_mass = m0 + target * wt;
+                        target -= 1;
+                        tie_val = to;
+                        tie = done = true;
+                    }
+                }
+                half ^= 1;  // another CTA may still read this list
+            }
+            if (!whole) have = false;
+            if (!tie) continue;
+        }
+
+        // The first element, in index order, whose running sum of weights (ties: of ones) exceeds
+        // the target; for the token, min(floor(u * sum), sum - 1).
+        const float under = tie ? tie_val : row.cut_val;
+        auto weigh = [&](const float4& x, int i, u64 (&v)[4]) {
+            const float l[4] = {x.x, x.y, x.z, x.w};
+            bool ok[4];
+#pragma unroll
+            for (int e = 0; e < 4; e++) ok[e] = row.kept(l[e], i + e);
+            if (tie) {
+#pragma unroll
+                for (int e = 0; e < 4; e++) v[e] = ok[e] && l[e] == tie_val ? 1 : 0;
+            } else {
+                row.weight4(l, ok, v);
+            }
+        };
+        const int per = ((n + SMP_WARPS - 1) / SMP_WARPS + 3) & ~3;  // a warp's contiguous share
+        u64 s = 0;
+        row.each(min(n, w * per), min(n, w * per + per), lane, 32, [&](const float4& x, int i) {
+            if (!(fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w)) >= under)) return;
+            u64 v[4];
+            weigh(x, i, v);
+            s += (v[0] + v[1]) + (v[2] + v[3]);
+        });
+        s = smp_warp_sum(s);
+        __syncthreads();
+        if (lane == 0) sm.red[0][w] = s;
+        __syncthreads();
+        const u64 mine = smp_warp_sum(lane < SMP_WARPS ? sm.red[0][lane] : 0ull);
+        const u64(*box)[SMP_MAX_CLUSTER] = row.exchange(mine, 0, 0, 0);
+        const u64 of = lane < C ? box[0][lane] : 0;
+        const u64 total = smp_warp_sum(of), before = smp_warp_sum(lane < r ? of : 0);
+        if (!tie) {
+            target = (u64)((double)u * (double)total);
+            if (target >= total) target = total - 1;
+        }
+        if (target >= before && target - before < mine) {  // in this CTA's slice (uniform)
+            u64 run = before;
+            int wi = 0;
+            while (run + sm.red[0][wi] <= target) run += sm.red[0][wi++];
+            const int from = min(n, wi * per), to = min(n, from + per);
+            for (int i0 = from; i0 < to; i0 += 4 * SMP_THREADS) {
+                const int i = i0 + 4 * (int)threadIdx.x;
+                u64 v[4] = {0, 0, 0, 0};
+                float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (i < to) {
+                    x = i < row.cached ? *reinterpret_cast<const float4*>(smp_cache() + i) : row.load4(i);
+                    weigh(x, i, v);
+                }
+                const u64 sum = (v[0] + v[1]) + (v[2] + v[3]);
+                const u64 inc = smp_warp_scan(sum, lane);
+                __syncthreads();
+                if (lane == 31) sm.red[1][w] = inc;
+                __syncthreads();
+                const u64 y = lane < SMP_WARPS ? sm.red[1][lane] : 0;
+                u64 upto = run + inc - sum + smp_warp_sum(lane < w ? y : 0);
+                run += smp_warp_sum(y);
+                const float xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    if (v[e] != 0 && upto <= target && upto + v[e] > target) {  // one thread of the row
+                        const uint32_t at = row.index(i + e);
+                        if (tie) {
+                            const u64 code = ((u64)smp_key(tie_val) << 32) | (uint32_t)~at;
+                            for (int t = 0; t < C; t++) *cl.map_shared_rank(&sm.cut, t) = code;
+                        } else {
+                            report(xs[e], at);
+                        }
+                    }
+                    upto += v[e];
+                }
+            }
+        }
+        if (!tie) return;  // after the exchange no CTA reads or writes another's memory
+        if (threadIdx.x == 0) sm.kept_mass = tie_mass;
+        cl.sync();
+        row.cut_at(sm.cut);
+        cut_mass = true;
+    }
 }
 
 }  // namespace dllm

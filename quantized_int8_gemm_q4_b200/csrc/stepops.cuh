@@ -259,7 +259,8 @@ int dllm_sample(const float* logits, int64_t R, int64_t V, int64_t ldl, const fl
     if (rc) return rc;
     const size_t most = 227 * 1024;
     if (!g_sample_attr_done[dev]) {
-        if (cudaFuncSetAttribute(sample_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) != cudaSuccess)
+        if (cudaFuncSetAttribute(sample_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) != cudaSuccess ||
+            cudaFuncSetAttribute(sample_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
             return DLLM_ERR_CUDA;
         g_sample_attr_done[dev] = true;
     }
@@ -271,8 +272,12 @@ int dllm_sample(const float* logits, int64_t R, int64_t V, int64_t ldl, const fl
     a.token = token, a.conf = conf, a.entropy = entropy;
     int C = 1;
     while (C < 8 && (int64_t)C * 8192 < V) C *= 2;
+    if (C == 8 && 16 * R <= g_num_sms[dev]) C = 16;
     a.slice = (int32_t)round_up((V + 3 + C - 1) / C, 128);
-    const int64_t room = (int64_t)((most - sizeof(SampleShared)) / 16 * 4);
+    // Two CTAs per SM where at least 3/4 of a slice then fits in shared memory (the rest is
+    // read again from L2), else one.
+    const int64_t pair = (int64_t)((112 * 1024 - sizeof(SampleShared)) / 16 * 4);
+    const int64_t room = 4 * pair >= 3 * (int64_t)a.slice ? pair : (int64_t)((most - sizeof(SampleShared)) / 16 * 4);
     a.cached = (int32_t)(a.slice < room ? a.slice : room);
     int bits = 0;
     while ((1LL << bits) < V) bits++;
