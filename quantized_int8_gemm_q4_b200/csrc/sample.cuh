@@ -34,11 +34,11 @@
 
 namespace dllm {
 
-constexpr int SMP_THREADS = 512;
+constexpr int SMP_THREADS = 256;
 constexpr int SMP_WARPS = SMP_THREADS / 32;
 constexpr int SMP_BINS = 2048;
 constexpr int SMP_COARSE = SMP_BINS / 32;
-constexpr int SMP_LIST = SMP_THREADS / 2;  // elements ranked exactly
+constexpr int SMP_LIST = SMP_THREADS;  // elements ranked exactly, one per thread
 constexpr int SMP_MAX_CLUSTER = 16;
 constexpr int SMP_TABLE = 256;
 constexpr int ERR_LOGITS = -10;
@@ -213,7 +213,11 @@ struct SampleRow {
 #pragma unroll
         for (int e = 0; e < 4; e++) v[e] = weight_of(t[e]);
 #pragma unroll
-        for (int e = 0; e < 4; e++) v[e] = ok[e] && v[e] >= min_w ? v[e] : 0;
+        for (int e = 0; e < 4; e++) v[e] = ok[e] ? v[e] : 0;
+        if (min_w != 0) {  // uniform
+#pragma unroll
+            for (int e = 0; e < 4; e++) v[e] = v[e] >= min_w ? v[e] : 0;
+        }
     }
     __device__ __forceinline__ u64 weight1(float l) const {
         const double t = coarse ? fmax(((double)l - (double)top) * scale, floor_t)
@@ -269,6 +273,7 @@ struct SampleRow {
         inv = (float)SMP_BINS / span;
         shift = max(0, 32 - __clz(smp_key(hi) - smp_key(lo)) - 11);
         linear = by_value && span > 0.0f && inv < 1e30f;
+        const bool uncut = by_value && low_i == INT_MAX;  // every value from lo up is a candidate
         if (clear) {
             for (int i = threadIdx.x; i < SMP_BINS; i += SMP_THREADS) sm.cnt[i] = sm.lo[i] = sm.hi[i] = 0;
             __syncthreads();
@@ -277,7 +282,7 @@ struct SampleRow {
             const float l[4] = {x.x, x.y, x.z, x.w};
             bool ok[4];
 #pragma unroll
-            for (int e = 0; e < 4; e++) ok[e] = in_range(l[e], i + e);
+            for (int e = 0; e < 4; e++) ok[e] = uncut ? l[e] >= lo : in_range(l[e], i + e);
             if (!(ok[0] | ok[1] | ok[2] | ok[3])) return;
             u64 v[4];
             if (mass) weight4(l, ok, v);
@@ -412,10 +417,8 @@ __global__ void __launch_bounds__(SMP_THREADS, 2) sample_kernel(const __grid_con
         sm.scale = 1.4426950408889634 / Td;
         sm.ln_min_p = min_p > 0.0 ? log(min_p) : 0.0;
     }
-    if (threadIdx.x >= SMP_THREADS - SMP_TABLE) {
-        const int i = threadIdx.x - (SMP_THREADS - SMP_TABLE);
-        sm.table[i] = exp2((double)i / SMP_TABLE + a.fix);
-    }
+    static_assert(SMP_TABLE == SMP_THREADS, "one entry per thread");
+    sm.table[threadIdx.x] = exp2((double)threadIdx.x / SMP_TABLE + a.fix);
     for (int i = threadIdx.x; i < SMP_BINS; i += SMP_THREADS) sm.cnt[i] = sm.lo[i] = sm.hi[i] = 0;
     __syncthreads();  // the barrier and the edges are there
     {
