@@ -60,12 +60,12 @@ struct SampleArgs {
 };
 
 struct alignas(16) SampleShared {  // the slice follows it, read in 16-byte vectors
+    ulonglong2 list[SMP_LIST];                           // all CTAs' elements of a gathered bin: order code, weight
     uint32_t cnt[SMP_BINS], lo[SMP_BINS], hi[SMP_BINS];  // this CTA's histogram: count, mass
     uint32_t ccnt[SMP_MAX_CLUSTER][SMP_COARSE];          // every CTA's coarse sums
     u64 cmass[SMP_MAX_CLUSTER][SMP_COARSE];
     u64 before_c[SMP_COARSE + 1], before_m[SMP_COARSE + 1];  // the cluster's, before each coarse bin
     u64 mine[2][SMP_LIST];                               // this CTA's elements of a gathered bin: order codes
-    u64 lcode[SMP_LIST], lw[SMP_LIST];                   // all of them, and their weights
     u64 box[2][4][SMP_MAX_CLUSTER];                      // one exchange: words of every CTA
     u64 plain[3][SMP_MAX_CLUSTER];                       // every CTA's sums of the plain softmax
     u64 red[4][SMP_WARPS];
@@ -595,25 +595,25 @@ __global__ void __launch_bounds__(SMP_THREADS, 2) sample_kernel(const __grid_con
                                 SampleShared* o = cl.map_shared_rank(&sm, 0);
                                 const uint32_t slot = atomicAdd(&o->n_list, 1u);
                                 if (slot < SMP_LIST)
-                                    o->lcode[slot] = ((u64)smp_key(l[e]) << 32) | (uint32_t)~row.index(i + e);
+                                    o->list[slot].x = ((u64)smp_key(l[e]) << 32) | (uint32_t)~row.index(i + e);
                             }
                     });
                     cl.sync();
                     if (r != 0) return;  // nothing of this CTA's memory is read from here on
                     const int m = (int)min(sm.n_list, (uint32_t)SMP_LIST), e = (int)threadIdx.x;
-                    const u64 code = e < m ? sm.lcode[e] : 0;
+                    const u64 code = e < m ? sm.list[e].x : 0;
                     const float l = smp_value((uint32_t)(code >> 32));
                     u64 weight = e < m ? row.weight1(l) : 0;
-                    if (e < m) sm.lw[e] = weight;
+                    if (e < m) sm.list[e].y = weight;
                     __syncthreads();
                     uint32_t rank = 0;
                     u64 pre = 0;
                     if (e < m) {
 #pragma unroll 4
                         for (int j = 0; j < m; j++) {
-                            const u64 other = sm.lcode[j], y = sm.lw[j];
-                            rank += other > code;
-                            pre += other > code ? y : 0;
+                            const ulonglong2 y = sm.list[j];
+                            rank += y.x > code;
+                            pre += y.x > code ? y.y : 0;
                         }
                     }
                     auto block_sum = [&](u64 y) {
@@ -632,7 +632,7 @@ __global__ void __launch_bounds__(SMP_THREADS, 2) sample_kernel(const __grid_con
                     in = in && (!by_p || pre < limit);
                     if (!in) weight = 0;
                     __syncthreads();
-                    if (e < m) sm.lw[e] = weight;
+                    if (e < m) sm.list[e].y = weight;
                     const u64 total = block_sum(weight);
                     target = (u64)((double)u * (double)total);
                     if (target >= total) target = total - 1;
@@ -641,8 +641,8 @@ __global__ void __launch_bounds__(SMP_THREADS, 2) sample_kernel(const __grid_con
                         const uint32_t at = (uint32_t)code;  // complement of the index
 #pragma unroll 4
                         for (int j = 0; j < m; j++) {
-                            const u64 y = sm.lw[j];
-                            run += (uint32_t)sm.lcode[j] > at ? y : 0;
+                            const ulonglong2 y = sm.list[j];
+                            run += (uint32_t)y.x > at ? y.y : 0;
                         }
                         if (run <= target && target - run < weight) report(l, ~at);
                     }
@@ -687,8 +687,8 @@ __global__ void __launch_bounds__(SMP_THREADS, 2) sample_kernel(const __grid_con
                     u64 code = 0;
                     if ((int)threadIdx.x < m) {
                         code = cl.map_shared_rank(&sm, source)->mine[half][slot];
-                        sm.lcode[e] = code;
-                        sm.lw[e] = mass ? row.weight1(smp_value((uint32_t)(code >> 32))) : 0;
+                        sm.list[e].x = code;
+                        sm.list[e].y = mass ? row.weight1(smp_value((uint32_t)(code >> 32))) : 0;
                     }
                     __syncthreads();
                     uint32_t rank = 0;
@@ -697,17 +697,17 @@ __global__ void __launch_bounds__(SMP_THREADS, 2) sample_kernel(const __grid_con
                     if ((int)threadIdx.x < m) {
 #pragma unroll 4
                         for (int j = 0; j < m; j++) {
-                            const u64 other = sm.lcode[j], weight = sm.lw[j];
-                            rank += other > code;
-                            pre += other > code ? weight : 0;
+                            const ulonglong2 y = sm.list[j];
+                            rank += y.x > code;
+                            pre += y.x > code ? y.y : 0;
                         }
                         // what weighs nothing is no candidate where masses count
-                        in = (by_count ? c0 + rank : pre) < limit && (!mass || sm.lw[e] != 0);
+                        in = (by_count ? c0 + rank : pre) < limit && (!mass || sm.list[e].y != 0);
                     }
                     const uint32_t last = __reduce_max_sync(0xffffffffu, in ? rank + 1 : 0);
                     if (lane == 0 && last) atomicMax(&sm.best, last);
                     __syncthreads();
-                    if (in && rank + 1 == sm.best) sm.cut = code, sm.kept_mass = pre + sm.lw[e];
+                    if (in && rank + 1 == sm.best) sm.cut = code, sm.kept_mass = pre + sm.list[e].y;
                     __syncthreads();
                     row.cut_at(sm.cut);
                     cut_mass = true;
