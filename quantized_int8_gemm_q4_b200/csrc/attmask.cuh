@@ -11,13 +11,16 @@
 // which is the order in which one TMA box of gp heads x 128 / gp rows lands in shared memory.  So
 // grouped heads read their keys once, and one query of 8 heads fills 8 rows.  A CTA has two
 // tiles (one for small grids) and the key blocks of 128 that any of their rows sees, or one of
-// `splits` equal parts of them; 12 warps:
-//   warps 0-3, 4-7  softmax of tile 0, tile 1; thread = row, all 128 scores of a block in
-//                   registers
-//   warp 8          one thread issues every MMA (S = Q K^T, O += P V; kind::f16, f32 in
+// `splits` equal parts of them; 20 warps:
+//   warps 0-7, 8-15 softmax of tile 0, tile 1; of a tile's eight, the first four take the
+//                   keys (and head-dim columns of O) 0..63 and the others 64..127 of the
+//                   same rows.  The two threads of a row agree on its running maximum m: a
+//                   barrier of their two warps tells whether any row must raise it (by more
+//                   than 2^8), and only then do they swap their maxima through shared memory.
+//   warp 16         one thread issues every MMA (S = Q K^T, O += P V; kind::f16, f32 in
 //                   tensor memory); the warp owns tensor memory
-//   warp 9, 10      TMA producers of Q and K, of V (two slots each, 128 keys x dh)
-//   warp 11         V's gate: in a block that some row does not see whole, it replaces what
+//   warp 17, 18     TMA producers of Q and K, of V (two slots each, 128 keys x dh)
+//   warp 19         V's gate: in a block that some row does not see whole, it replaces what
 //                   is not finite by zeros and marks those keys (a weight of zero times NaN is
 //                   NaN, and the hidden key of one row is another's); a row that attends a
 //                   marked key becomes NaN
@@ -35,19 +38,21 @@
 
 namespace dllm {
 
-constexpr int MSK_MMA_WARP = 8, MSK_K_WARP = 9, MSK_V_WARP = 10, MSK_GATE_WARP = 11;
-constexpr int MSK_THREADS = 32 * 12;
+constexpr int MSK_SOFTMAX_WARPS = 16;
+constexpr int MSK_MMA_WARP = 16, MSK_K_WARP = 17, MSK_V_WARP = 18, MSK_GATE_WARP = 19;
+constexpr int MSK_THREADS = 32 * 20;
 constexpr int MSK_BK = 128;  // keys per block
 // Registers per thread after setmaxnreg (softmax warpgroups; the others), out of the
-// launch's 384 x 168.
-constexpr int MSK_REG_SOFTMAX = 200, MSK_REG_OTHER = 96, MSK_REG_LAUNCH = 168;
-static_assert(256 * MSK_REG_SOFTMAX + 128 * MSK_REG_OTHER <= MSK_THREADS * MSK_REG_LAUNCH, "setmaxnreg split");
+// launch's 640 x 96.
+constexpr int MSK_REG_SOFTMAX = 104, MSK_REG_OTHER = 64, MSK_REG_LAUNCH = 96;
+static_assert(512 * MSK_REG_SOFTMAX + 128 * MSK_REG_OTHER <= MSK_THREADS * MSK_REG_LAUNCH, "setmaxnreg split");
 
 struct MaskShared {
     uint64_t q_full[2], k_full[2], v_full[2], v_ready[2], k_empty[2], v_empty[2];
     uint64_t s_full[2], p_full[2], o_done[2], fin;
     uint32_t tmem, flags[2][4];  // per V slot, bit j: key j's value is not finite
-    int32_t lo_min[8], hi_max[8], lo_max[8], hi_min[8];  // per softmax warp, over rows with keys
+    int32_t lo_min[8], hi_max[8], lo_max[8], hi_min[8];  // per tile and quadrant, over rows with keys
+    float swap[2][2][128];  // per tile and half: a row's block maximum; at the end its sum
 };
 // Q x2, K x2, V x2, barriers
 constexpr size_t MSK_SMEM = 6 * (size_t)ATT_TILE + sizeof(MaskShared);
@@ -115,7 +120,7 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
             mbar_init(&sh.k_empty[b], 1);
             mbar_init(&sh.v_empty[b], 1);
             mbar_init(&sh.s_full[b], 1);
-            mbar_init(&sh.p_full[b], 4);
+            mbar_init(&sh.p_full[b], 8);
             mbar_init(&sh.o_done[b], 1);
         }
         mbar_init(&sh.fin, 1);
@@ -130,10 +135,10 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
     pdl_wait();  // q, k, v and the intervals may come from the previous kernel on the stream
 
     // This thread's row (softmax warps): query, head, interval.
-    const int t = warp >> 2, row = threadIdx.x & 127;
+    const int t = warp >> 3, half = (warp >> 2) & 1, quad = warp & 3, row = threadIdx.x & 127;
     int qi = 0, head = 0, lo = 0, hi = 0;
     bool live = false;
-    if (warp < 8) {
+    if (warp < MSK_SOFTMAX_WARPS) {
         qi = q0 + t * a.tq + row / a.gp;
         head = h0 + row % a.gp;
         live = t < ntiles && row < a.tq * a.gp && qi < a.Lq;
@@ -144,7 +149,8 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
         const bool some = live && lo < hi;
         const int l0 = __reduce_min_sync(~0u, some ? lo : INT_MAX), h1 = __reduce_max_sync(~0u, some ? hi : 0);
         const int l1 = __reduce_max_sync(~0u, some ? lo : 0), h2 = __reduce_min_sync(~0u, some ? hi : INT_MAX);
-        if (lane == 0) sh.lo_min[warp] = l0, sh.hi_max[warp] = h1, sh.lo_max[warp] = l1, sh.hi_min[warp] = h2;
+        const int at = 4 * t + quad;
+        if (lane == 0 && half == 0) sh.lo_min[at] = l0, sh.hi_max[at] = h1, sh.lo_max[at] = l1, sh.hi_min[at] = h2;
     }
     tc_fence_before();
     __syncthreads();
@@ -177,7 +183,7 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
     // A block that every row of both tiles sees whole needs no gate.
     auto whole = [&](int kb) { return kb * MSK_BK >= b_full0 && (kb + 1) * MSK_BK <= b_full1; };
 
-    if (warp >= 8) {
+    if (warp >= MSK_SOFTMAX_WARPS) {
         setmaxnreg_dec<MSK_REG_OTHER>();
         if (warp == MSK_K_WARP || warp == MSK_V_WARP) {
             // ------------------------------------------------------------ TMA producers
@@ -216,17 +222,25 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
                     if (lane < 4) sh.flags[b][lane] = 0;
                     __syncwarp();
                     uint4* const v = reinterpret_cast<uint4*>(sV + b * ATT_TILE);
-#pragma unroll 8
-                    for (int i = lane; i < ATT_TILE / 16; i += 32) {
-                        const uint4 x = v[i];
-                        // an f16 with all exponent bits set carries into its sign bit
-                        auto c = [](uint32_t y) { return (y & 0x7fff7fffu) + 0x04000400u; };
-                        if ((c(x.x) | c(x.y) | c(x.z) | c(x.w)) & 0x80008000u) {
-                            auto z = [&](uint32_t y) {
-                                const uint32_t m = (c(y) & 0x80008000u) >> 15;  // 1 per half to clear
-                                return y & ~(m * 0xffffu);
+                    // an f16 with all exponent bits set carries into its sign bit
+                    auto c = [](uint32_t y) { return (y & 0x7fff7fffu) + 0x04000400u; };
+#pragma unroll 1
+                    for (int i0 = lane; i0 < ATT_TILE / 16; i0 += 8 * 32) {
+                        uint4 x[8];
+#pragma unroll
+                        for (int e = 0; e < 8; e++) x[e] = v[i0 + 32 * e];
+                        uint32_t any = 0;
+#pragma unroll
+                        for (int e = 0; e < 8; e++) any |= c(x[e].x) | c(x[e].y) | c(x[e].z) | c(x[e].w);
+                        if (!(any & 0x80008000u)) continue;
+                        for (int i = i0; i < i0 + 8 * 32; i += 32) {
+                            const uint4 y = v[i];
+                            auto z = [&](uint32_t u) {
+                                const uint32_t m = (c(u) & 0x80008000u) >> 15;  // 1 per half to clear
+                                return u & ~(m * 0xffffu);
                             };
-                            v[i] = make_uint4(z(x.x), z(x.y), z(x.z), z(x.w));
+                            if (!((c(y.x) | c(y.y) | c(y.z) | c(y.w)) & 0x80008000u)) continue;
+                            v[i] = make_uint4(z(y.x), z(y.y), z(y.z), z(y.w));
                             const int key = (i >> 3) & 127;  // 128-byte rows of 64 head-dim values
                             atomicOr(&sh.flags[b][key >> 5], 1u << (key & 31));
                         }
@@ -245,12 +259,12 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
             // One step beyond the last block: its P V only.
             for (int n = 0; ok && n <= B1 - B0; n++) {
                 const int kb = B0 + n, b = n & 1;
-#pragma unroll 1
-                for (int x = 0; ok && x < 2; x++) {
+#pragma unroll
+                for (int x = 0; x < 2; x++) {
                     const uint32_t tO = tm + 256 * x, tS = tO + 128;
-                    if (n > 0 && kb - 1 >= t0[x] && kb - 1 < t1[x]) {
+                    if (ok && n > 0 && kb - 1 >= t0[x] && kb - 1 < t1[x]) {
                         const int p = b ^ 1;  // slot of block kb - 1
-                        ok = att_wait(&sh.p_full[x], (kb - 1 - t0[x]) & 1) && att_wait(&sh.v_ready[p], ((n - 1) >> 1) & 1);
+                        ok = ok && att_wait(&sh.p_full[x], (kb - 1 - t0[x]) & 1) && att_wait(&sh.v_ready[p], ((n - 1) >> 1) & 1);
                         if (!ok) break;
                         tc_fence_after();
                         const uint64_t d = dv + (uint64_t)(p * (ATT_TILE >> 4));
@@ -259,7 +273,7 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
                         for (int kk = 1; kk < MSK_BK / 16; kk++) mma_f16_ts(tO, tS + 8 * kk, d + att_v_step(kk), ID_O, 1);
                         if (kb == t1[x]) tc_commit(&sh.o_done[x]);
                     }
-                    if (kb >= t0[x] && kb < t1[x]) {
+                    if (ok && kb >= t0[x] && kb < t1[x]) {
                         ok = (kb > t0[x] || att_wait(&sh.q_full[x], 0)) && att_wait(&sh.k_full[b], (n >> 1) & 1);
                         if (!ok) break;
                         tc_fence_after();
@@ -289,8 +303,11 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
     } else {
         // ---------------------------------------------------------------- softmax, output
         setmaxnreg_inc<MSK_REG_SOFTMAX>();
-        const uint32_t tO = tm + ((uint32_t)(32 * (warp & 3)) << 16) + 256 * t, tS = tO + 128;
-        const int w_lo0 = sh.lo_min[warp], w_hi1 = sh.hi_max[warp], w_lo1 = sh.lo_max[warp], w_hi0 = sh.hi_min[warp];
+        const uint32_t tl = tm + ((uint32_t)(32 * quad) << 16) + 256 * t;
+        const uint32_t tO = tl + 64 * half, tS = tl + 128 + 64 * half, tP = tl + 128 + 32 * half;
+        const int kb0 = t ? t0[1] : t0[0], kb1 = t ? t1[1] : t1[0];
+        const int sw = 4 * t + quad, bar = 1 + sw;
+        const int w_lo0 = sh.lo_min[sw], w_hi1 = sh.hi_max[sw], w_lo1 = sh.lo_max[sw], w_hi0 = sh.hi_min[sw];
         const bool some = lo < hi;
         if (!some) lo = 0, hi = a.Lk;  // a row without keys runs along; it stores zeros
         float slope = 0.0f;
@@ -300,70 +317,71 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
             qp = a.q_pos ? __ldg(a.q_pos + qi) : qi + a.Lk - a.Lq;
         }
         float m = -INFINITY, l = 0.0f;
-        bool ok = true;
-        for (int kb = t0[t]; kb < t1[t]; kb++) {
-            ok = __all_sync(~0u, att_wait(&sh.s_full[t], (kb - t0[t]) & 1));
-            if (!ok) break;
-            tc_fence_after();
-            const int k0 = kb * MSK_BK;
-            if (k0 >= w_hi1 || k0 + MSK_BK <= w_lo0) {  // no row of the warp sees the block
+        bool ok = true;  // alike in the two warps of a row after every barrier of theirs
+        for (int kb = kb0; kb < kb1; kb++) {
+            ok = __all_sync(~0u, att_wait(&sh.s_full[t], (kb - kb0) & 1));
+            if (ok) tc_fence_after();
+            const int k0 = kb * MSK_BK + 64 * half;  // this half's first key
+            if (kb * MSK_BK >= w_hi1 || (kb + 1) * MSK_BK <= w_lo0) {  // no row of the two warps sees the block
+                ok = named_barrier_and(bar, 64, ok);  // the two warps stop together or not at all
+                if (!ok) break;
                 uint32_t z[16];
 #pragma unroll
                 for (int e = 0; e < 16; e++) z[e] = 0u;
-#pragma unroll
-                for (int c = 0; c < 4; c++) tmem_st16(tS + 16 * c, z);
+                tmem_st16(tP, z);
+                tmem_st16(tP + 16, z);
             } else {
-                float s[MSK_BK];
+                float s[64];
+                if (ok) {
 #pragma unroll
-                for (int c = 0; c < 8; c++) tmem_ld16(tS + 16 * c, reinterpret_cast<uint32_t*>(s) + 16 * c);
-                tmem_wait_ld();
+                    for (int c = 0; c < 4; c++) tmem_ld16(tS + 16 * c, reinterpret_cast<uint32_t*>(s) + 16 * c);
+                    tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 64; j++) s[j] = 0.0f;
+                }
                 if constexpr (CAP) {
 #pragma unroll
-                    for (int j = 0; j < MSK_BK; j++) s[j] = a.cap_out * att_tanh(s[j] * a.cap_in);
+                    for (int j = 0; j < 64; j++) s[j] = a.cap_out * att_tanh(s[j] * a.cap_in);
                 } else if constexpr (BIAS) {
 #pragma unroll
-                    for (int j = 0; j < MSK_BK; j++) s[j] *= ATT_C;
+                    for (int j = 0; j < 64; j++) s[j] *= ATT_C;
                 }
                 if constexpr (BIAS) {
                     const float d = (float)((int64_t)qp - k0);
 #pragma unroll
-                    for (int j = 0; j < MSK_BK; j++) s[j] = fmaf(-slope, fabsf(d - (float)j), s[j]);
+                    for (int j = 0; j < 64; j++) s[j] = fmaf(-slope, fabsf(d - (float)j), s[j]);
                 }
-                if (k0 < w_lo1 || k0 + MSK_BK > w_hi0) {  // warp-uniform: some row hides some key
+                if (k0 < w_lo1 || k0 + 64 > w_hi0) {  // warp-uniform: some row hides some key
                     const int from = lo - k0, n = hi - lo;
 #pragma unroll
-                    for (int j = 0; j < MSK_BK; j++)
+                    for (int j = 0; j < 64; j++)
                         if ((uint32_t)(j - from) >= (uint32_t)n) s[j] = -INFINITY;
                 }
-                if (!whole(kb)) {  // the gate has looked at V: a marked key of the row's own?
-                    const int b = (kb - B0) & 1;
-                    ok = __all_sync(~0u, att_wait(&sh.v_ready[b], ((kb - B0) >> 1) & 1));
-                    if (!ok) break;
-#pragma unroll 1
-                    for (int w = 0; w < 4; w++)
-                        for (uint32_t f = sh.flags[b][w]; f; f &= f - 1)
-                            if ((uint32_t)(k0 + 32 * w + __ffs(f) - 1 - lo) < (uint32_t)(hi - lo)) l = NAN;
-                }
-                float mx[8];
+                float mx[4];
 #pragma unroll
-                for (int e = 0; e < 8; e++) mx[e] = s[e];
+                for (int e = 0; e < 4; e++) mx[e] = fmaxf(s[e], s[4 + e]);
 #pragma unroll
-                for (int j = 8; j < MSK_BK; j += 16)
+                for (int j = 8; j < 64; j += 8)
 #pragma unroll
-                    for (int e = 0; e < 8; e++)
-                        mx[e] = j + 8 + e < MSK_BK ? max3f(mx[e], s[j + e], s[j + 8 + e]) : fmaxf(mx[e], s[j + e]);
-                float top = max3f(max3f(mx[0], mx[1], mx[2]), max3f(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+                    for (int e = 0; e < 4; e++) mx[e] = max3f(mx[e], s[j + e], s[j + 4 + e]);
                 constexpr float C = CAP || BIAS ? 1.0f : ATT_C;
-                top *= C;
-                const bool raise = top > m + ATT_RESCALE_LOG2;  // also from -inf; not where all is hidden
-                if (__any_sync(~0u, raise)) {
+                float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * C;
+                // Both warps have S in registers after this barrier: P may be written over it.
+                const bool calm = named_barrier_and(bar, 64, ok && !(top > m + ATT_RESCALE_LOG2));
+                if (!calm) {
+                    sh.swap[t][half][row] = top;
+                    ok = named_barrier_and(bar, 64, ok);
+                    if (!ok) break;
+                    top = fmaxf(top, sh.swap[t][half ^ 1][row]);
+                    const bool raise = top > m + ATT_RESCALE_LOG2;  // also from -inf; not where all is hidden
                     // S(kb) is committed after P V(kb - 1): O is complete
                     const float alpha = raise ? att_ex2(m - top) : 1.0f;  // 0 from -inf
                     if (raise) m = top;
                     l *= alpha;
-                    if (kb > t0[t]) {
+                    if (kb > kb0) {
 #pragma unroll 1
-                        for (int c = 0; c < 8; c++) {
+                        for (int c = 0; c < 4; c++) {
                             uint32_t r[16];
                             tmem_ld16(tO + 16 * c, r);
                             tmem_wait_ld();
@@ -375,11 +393,10 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
                 }
                 const float neg = m == -INFINITY ? 0.0f : -m;
                 const float2 c2 = make_float2(C, C), n2 = make_float2(neg, neg);
-                float2 sum[4];
+                float2 sum[2];
+                sum[0] = sum[1] = make_float2(0.0f, 0.0f);
 #pragma unroll
-                for (int e = 0; e < 4; e++) sum[e] = make_float2(0.0f, 0.0f);
-#pragma unroll
-                for (int c = 0; c < 4; c++) {
+                for (int c = 0; c < 2; c++) {
                     uint32_t pk[16];
 #pragma unroll
                     for (int e = 0; e < 16; e++) {
@@ -387,49 +404,64 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
                         x = CAP || BIAS ? fadd2(x, n2) : ffma2(x, c2, n2);
                         x.x = att_ex2(x.x);
                         x.y = att_ex2(x.y);
-                        sum[e & 3] = fadd2(sum[e & 3], x);
+                        sum[e & 1] = fadd2(sum[e & 1], x);
                         pk[e] = pack_h2(x.x, x.y);
                     }
-                    tmem_st16(tS + 16 * c, pk);
+                    tmem_st16(tP + 16 * c, pk);
                 }
-                const float2 u = fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3]));
+                const float2 u = fadd2(sum[0], sum[1]);
                 l += u.x + u.y;
             }
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.p_full[t]);
+            if (!whole(kb) && !(kb * MSK_BK >= w_hi1 || (kb + 1) * MSK_BK <= w_lo0)) {
+                // the gate has looked at V: a marked key of the row's own?
+                const int b = (kb - B0) & 1;
+                if (!__all_sync(~0u, att_wait(&sh.v_ready[b], ((kb - B0) >> 1) & 1))) l = NAN;
+#pragma unroll 1
+                for (int w = 2 * half; w < 2 * half + 2; w++)
+                    for (uint32_t f = sh.flags[b][w]; f; f &= f - 1)
+                        if ((uint32_t)(kb * MSK_BK + 32 * w + __ffs(f) - 1 - lo) < (uint32_t)(hi - lo)) l = NAN;
+            }
         }
-        const bool ran = t0[t] < t1[t];
+        const bool ran = kb0 < kb1;
         if (ran && ok) ok = __all_sync(~0u, att_wait(&sh.o_done[t], 0));
+        if (ran) {
+            sh.swap[t][half][row] = l;
+            ok = named_barrier_and(bar, 64, ok);
+            l += sh.swap[t][half ^ 1][row];
+        }
         if (ok) {
             tc_fence_after();
             const int64_t at = (int64_t)qi * a.H + head;
             const bool split = a.splits > 1;
             const int64_t pat = (int64_t)blockIdx.y * a.Lq * a.H + at;
             const float inv = some && ran ? (split ? 1.0f : 1.0f / l) : 0.0f;
-            if (split && live) a.part_ml[pat] = some && ran ? make_float2(m, l) : make_float2(-INFINITY, 0.0f);
-#pragma unroll 1
-            for (int c = 0; c < 8; c++) {
-                float r[16];
+            if (split && live && half == 0) a.part_ml[pat] = some && ran ? make_float2(m, l) : make_float2(-INFINITY, 0.0f);
+#pragma unroll
+            for (int c = 0; c < 2; c++) {
+                float r[32];
                 if (ran) {
-                    tmem_ld16(tO + 16 * c, reinterpret_cast<uint32_t*>(r));
+                    tmem_ld16(tO + 32 * c, reinterpret_cast<uint32_t*>(r));
+                    tmem_ld16(tO + 32 * c + 16, reinterpret_cast<uint32_t*>(r) + 16);
                     tmem_wait_ld();
                 }
 #pragma unroll
-                for (int e = 0; e < 16; e++) r[e] = some && ran ? r[e] * inv : 0.0f;
+                for (int e = 0; e < 32; e++) r[e] = some && ran ? r[e] * inv : 0.0f;
                 if (!live || (split && !ran)) continue;
+                const int64_t col = 64 * half + 32 * c;
                 if (split || !a.o_f16) {
-                    float* dst = split ? a.part + pat * ATT_DH : static_cast<float*>(a.o) + at * ATT_DH;
+                    float* dst = (split ? a.part + pat * ATT_DH : static_cast<float*>(a.o) + at * ATT_DH) + col;
+#pragma unroll
+                    for (int e = 0; e < 8; e++)
+                        reinterpret_cast<float4*>(dst)[e] = make_float4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
+                } else {
+                    __half* dst = static_cast<__half*>(a.o) + at * ATT_DH + col;
 #pragma unroll
                     for (int e = 0; e < 4; e++)
-                        reinterpret_cast<float4*>(dst + 16 * c)[e] =
-                            make_float4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
-                } else {
-                    __half* dst = static_cast<__half*>(a.o) + at * ATT_DH;
-#pragma unroll
-                    for (int e = 0; e < 2; e++)
-                        reinterpret_cast<uint4*>(dst + 16 * c)[e] =
+                        reinterpret_cast<uint4*>(dst)[e] =
                             make_uint4(pack_h2(r[8 * e], r[8 * e + 1]), pack_h2(r[8 * e + 2], r[8 * e + 3]),
                                        pack_h2(r[8 * e + 4], r[8 * e + 5]), pack_h2(r[8 * e + 6], r[8 * e + 7]));
                 }
