@@ -10,27 +10,29 @@
 // (the largest divisor of the group up to 128) x 128 / gp queries, row = query * gp + head,
 // which is the order in which one TMA box of gp heads x 128 / gp rows lands in shared memory.  So
 // grouped heads read their keys once, and one query of 8 heads fills 8 rows.  A CTA has two
-// tiles (one for small grids) and the key blocks of 128 that any of their rows sees, or one of
-// `splits` equal parts of them; 20 warps:
-//   warps 0-7, 8-15 softmax of tile 0, tile 1; of a tile's eight, the first four take the
-//                   keys (and head-dim columns of O) 0..63 and the others 64..127 of the
-//                   same rows.  The two threads of a row agree on its running maximum m: a
-//                   barrier of their two warps tells whether any row must raise it (by more
-//                   than 2^8), and only then do they swap their maxima through shared memory.
-//   warp 16         one thread issues every MMA (S = Q K^T, O += P V; kind::f16, f32 in
-//                   tensor memory); the warp owns tensor memory
-//   warp 17, 18     TMA producers of Q and K, of V (two slots each, 128 keys x dh)
-//   warp 19         V's gate: in a block that some row does not see whole, it replaces what
+// tiles (one for small grids) and the key blocks of 64 that any of their rows sees, or one of
+// `splits` equal parts of them; 12 warps:
+//   warps 0-3, 4-7  softmax of tile 0, tile 1; thread = row, all 64 scores of a block in
+//                   registers; the running maximum is raised by more than 2^8 at a time
+//   warp 8, 9       issue the MMAs of tile 0, tile 1 (S = Q K^T, O += P V; kind::f16, f32 in
+//                   tensor memory); warp 8 owns tensor memory.  The whole warp runs the
+//                   issue loop and an elected lane's predicate guards each instruction, so
+//                   that its operands stay in uniform registers: 75-97 cycles per MMA from
+//                   one warp against 141 inside a one-lane branch; two warps together issue
+//                   one per 64, the tensor core's rate.
+//   warp 10         TMA producer of Q, K and V (four slots each of 64 keys x dh)
+//   warp 11         V's gate: in a block that some row does not see whole, it replaces what
 //                   is not finite by zeros and marks those keys (a weight of zero times NaN is
 //                   NaN, and the hidden key of one row is another's); a row that attends a
 //                   marked key becomes NaN
-// Issue order per block: P V of tile 0 (block kb - 1), S of tile 0 (kb), P V of tile 1, S of
-// tile 1: while one tile's softmax runs, the tensor core works on the other tile.  P lies
-// over its S in tensor memory (f16 pairs), so O_t and S_t of both tiles fill the 512 columns.
-// A commit after S(kb) also covers P V(kb - 1), so a thread that sees S may rescale O.
+// Tensor memory: O_t at columns 256 t, two S slots of 64 columns behind it, block kb in slot
+// kb & 1; P lies over the first half of its S (f16 pairs).  Issue order per tile: S(0), S(1), then
+// P V(kb), S(kb + 2): the scores of the next block are there when a softmax ends, and the
+// tensor core works while the softmax of either tile runs.
 //
-// Bounds per pair of tiles and block: 2048 cycles of MMA (4 x 8 of 128 x 128 x 16 at 8192
-// operations per cycle) and 2048 of the special-function unit (32768 exponentials at 16 per cycle).
+// Bounds per pair of tiles and 128 keys: 2048 cycles of MMA at 8192 operations per cycle (2600
+// as issued: a 128 x 64 x 16 MMA takes 49 cycles for its 6 KB of shared memory), and 2048 of the
+// special-function unit (32768 exponentials at 16 per cycle).
 #pragma once
 #include "attention.cuh"
 #include "qgemm.cuh"
@@ -38,24 +40,25 @@
 
 namespace dllm {
 
-constexpr int MSK_SOFTMAX_WARPS = 16;
-constexpr int MSK_MMA_WARP = 16, MSK_K_WARP = 17, MSK_V_WARP = 18, MSK_GATE_WARP = 19;
-constexpr int MSK_THREADS = 32 * 20;
-constexpr int MSK_BK = 128;  // keys per block
+constexpr int MSK_SOFTMAX_WARPS = 8;
+constexpr int MSK_MMA_WARP = 8, MSK_TMA_WARP = 10, MSK_GATE_WARP = 11;  // 8, 9: one per tile
+constexpr int MSK_THREADS = 32 * 12;
+constexpr int MSK_BK = 64;    // keys per block
+constexpr int MSK_SLOTS = 4;  // K and V slots
+constexpr int MSK_KV = MSK_BK * ATT_DH * 2;
 // Registers per thread after setmaxnreg (softmax warpgroups; the others), out of the
-// launch's 640 x 96.
-constexpr int MSK_REG_SOFTMAX = 104, MSK_REG_OTHER = 64, MSK_REG_LAUNCH = 96;
-static_assert(512 * MSK_REG_SOFTMAX + 128 * MSK_REG_OTHER <= MSK_THREADS * MSK_REG_LAUNCH, "setmaxnreg split");
+// launch's 384 x 168.
+constexpr int MSK_REG_SOFTMAX = 200, MSK_REG_OTHER = 96, MSK_REG_LAUNCH = 168;
+static_assert(256 * MSK_REG_SOFTMAX + 128 * MSK_REG_OTHER <= MSK_THREADS * MSK_REG_LAUNCH, "setmaxnreg split");
 
 struct MaskShared {
-    uint64_t q_full[2], k_full[2], v_full[2], v_ready[2], k_empty[2], v_empty[2];
-    uint64_t s_full[2], p_full[2], o_done[2], fin;
-    uint32_t tmem, flags[2][4];  // per V slot, bit j: key j's value is not finite
-    int32_t lo_min[8], hi_max[8], lo_max[8], hi_min[8];  // per tile and quadrant, over rows with keys
-    float swap[2][2][128];  // per tile and half: a row's block maximum; at the end its sum
+    uint64_t q_full[2], k_full[MSK_SLOTS], v_full[MSK_SLOTS], v_ready[MSK_SLOTS], k_empty[MSK_SLOTS], v_empty[MSK_SLOTS];
+    uint64_t s_full[2][2], p_full[2][2], o_done[2][2], fin;  // [tile][S slot]
+    uint32_t tmem, flags[MSK_SLOTS][2];  // per V slot, bit j: key j's value is not finite
+    int32_t lo_min[8], hi_max[8], lo_max[8], hi_min[8];  // per softmax warp, over rows with keys
 };
-// Q x2, K x2, V x2, barriers
-constexpr size_t MSK_SMEM = 6 * (size_t)ATT_TILE + sizeof(MaskShared);
+// Q x2, K x4, V x4, barriers
+constexpr size_t MSK_SMEM = 2 * (size_t)ATT_TILE + 2 * MSK_SLOTS * (size_t)MSK_KV + sizeof(MaskShared);
 
 struct MaskArgs {
     int32_t Lq, Lk, H, group;
@@ -87,6 +90,38 @@ __device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
     return *reinterpret_cast<float2*>(&d);
 }
 
+// One lane of a converged warp, as a predicate.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r;
+}
+// mma_f16_ss and mma_f16_ts where `issue` is not 0.
+__device__ __forceinline__ void mma_f16_ss_if(uint32_t issue, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                              uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(issue)
+        : "memory");
+}
+__device__ __forceinline__ void mma_f16_ts_if(uint32_t issue, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                              uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(issue)
+        : "memory");
+}
+
 // tanh(y) = 1 - 2 / (1 + 2^(2 log2(e) y)), good to a few 2^-24 absolute.
 __device__ __forceinline__ float att_tanh(float y) {
     const float e = att_ex2(y * 2.885390081777927f);
@@ -100,10 +135,10 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
                             const __grid_constant__ CUtensorMap tv, const __grid_constant__ MaskArgs a) {
     constexpr bool CAP = MODE & 1, BIAS = MODE & 2;
     extern __shared__ __align__(1024) uint8_t smem[];
-    uint8_t* const sQ = smem;                // two tiles
-    uint8_t* const sK = smem + 2 * ATT_TILE; // two slots
-    uint8_t* const sV = smem + 4 * ATT_TILE; // two slots
-    MaskShared& sh = *reinterpret_cast<MaskShared*>(smem + 6 * ATT_TILE);
+    uint8_t* const sQ = smem;                       // two tiles
+    uint8_t* const sK = smem + 2 * ATT_TILE;        // four slots
+    uint8_t* const sV = sK + MSK_SLOTS * MSK_KV;    // four slots
+    MaskShared& sh = *reinterpret_cast<MaskShared*>(sV + MSK_SLOTS * MSK_KV);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // The last queries first (under causal intervals theirs are the longest), all heads of them.
@@ -114,16 +149,20 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
     if (threadIdx.x == 32 * MSK_MMA_WARP) {
         for (int b = 0; b < 2; b++) {
             mbar_init(&sh.q_full[b], 1);
+            for (int x = 0; x < 2; x++) {
+                mbar_init(&sh.s_full[x][b], 1);
+                mbar_init(&sh.p_full[x][b], 4);
+                mbar_init(&sh.o_done[x][b], 1);
+            }
+        }
+        for (int b = 0; b < MSK_SLOTS; b++) {
             mbar_init(&sh.k_full[b], 1);
             mbar_init(&sh.v_full[b], 1);
             mbar_init(&sh.v_ready[b], 1);
-            mbar_init(&sh.k_empty[b], 1);
-            mbar_init(&sh.v_empty[b], 1);
-            mbar_init(&sh.s_full[b], 1);
-            mbar_init(&sh.p_full[b], 8);
-            mbar_init(&sh.o_done[b], 1);
+            mbar_init(&sh.k_empty[b], 2);  // both tiles' issuers
+            mbar_init(&sh.v_empty[b], 2);
         }
-        mbar_init(&sh.fin, 1);
+        mbar_init(&sh.fin, 2);
         fence_mbar_init();
     }
     if (warp == MSK_MMA_WARP) {
@@ -135,7 +174,7 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
     pdl_wait();  // q, k, v and the intervals may come from the previous kernel on the stream
 
     // This thread's row (softmax warps): query, head, interval.
-    const int t = warp >> 3, half = (warp >> 2) & 1, quad = warp & 3, row = threadIdx.x & 127;
+    const int t = warp >> 2, quad = warp & 3, row = threadIdx.x & 127;
     int qi = 0, head = 0, lo = 0, hi = 0;
     bool live = false;
     if (warp < MSK_SOFTMAX_WARPS) {
@@ -149,8 +188,7 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
         const bool some = live && lo < hi;
         const int l0 = __reduce_min_sync(~0u, some ? lo : INT_MAX), h1 = __reduce_max_sync(~0u, some ? hi : 0);
         const int l1 = __reduce_max_sync(~0u, some ? lo : 0), h2 = __reduce_min_sync(~0u, some ? hi : INT_MAX);
-        const int at = 4 * t + quad;
-        if (lane == 0 && half == 0) sh.lo_min[at] = l0, sh.hi_max[at] = h1, sh.lo_max[at] = l1, sh.hi_min[at] = h2;
+        if (lane == 0) sh.lo_min[warp] = l0, sh.hi_max[warp] = h1, sh.lo_max[warp] = l1, sh.hi_min[warp] = h2;
     }
     tc_fence_before();
     __syncthreads();
@@ -185,47 +223,54 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
 
     if (warp >= MSK_SOFTMAX_WARPS) {
         setmaxnreg_dec<MSK_REG_OTHER>();
-        if (warp == MSK_K_WARP || warp == MSK_V_WARP) {
-            // ------------------------------------------------------------ TMA producers
-            const bool is_k = warp == MSK_K_WARP;
-            const uint32_t q_bytes = (uint32_t)(a.gp * a.tq) * ATT_DH * 2;
-            const int nq = is_k && B0 < B1 ? ntiles : 0;
+        if (warp == MSK_TMA_WARP) {
+            // ------------------------------------------------------------ TMA producer
+            const int nq = B0 < B1 ? ntiles : 0;
             for (int x = 0; x < nq; x++) {
-                if (lane == 0) mbar_arrive_expect_tx(&sh.q_full[x], q_bytes);
+                if (lane == 0) mbar_arrive_expect_tx(&sh.q_full[x], (uint32_t)(a.gp * a.tq) * ATT_DH * 2);
                 __syncwarp();
                 att_tma_tile(sQ + x * ATT_TILE, &tq, h0, q0 + x * a.tq, &sh.q_full[x], lane);
             }
-            uint64_t* const full = is_k ? sh.k_full : sh.v_full;
-            uint64_t* const empty = is_k ? sh.k_empty : sh.v_empty;
-            const CUtensorMap* const tmap = is_k ? &tk : &tv;
-            uint8_t* const dst = is_k ? sK : sV;
-            int n = 0;
-            for (; n < B1 - B0; n++) {
-                const int b = n & 1;
-                if (n >= 2 && !__all_sync(~0u, att_wait(&empty[b], ((n >> 1) - 1) & 1))) break;
-                if (lane == 0) mbar_arrive_expect_tx(&full[b], ATT_TILE);
+            int nk = 0, nv = 0;
+            auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* full, int kb) {
+                if (lane == 0) mbar_arrive_expect_tx(full, MSK_KV);
                 __syncwarp();
-                att_tma_tile(dst + b * ATT_TILE, tmap, hk, (B0 + n) * MSK_BK, &full[b], lane);
+                if (lane < 2) tma_load_3d(dst + lane * (MSK_KV / 2), map, 64 * lane, hk, kb * MSK_BK, full);
+            };
+            for (int n = 0; n < B1 - B0; n++) {
+                const int b = n % MSK_SLOTS;
+                const uint32_t before = (n / MSK_SLOTS - 1) & 1;  // the slot's last use
+                if (n >= MSK_SLOTS && !__all_sync(~0u, att_wait(&sh.k_empty[b], before))) break;
+                load(sK + b * MSK_KV, &tk, &sh.k_full[b], B0 + n);
+                nk = n + 1;
+                if (n >= MSK_SLOTS && !__all_sync(~0u, att_wait(&sh.v_empty[b], before))) break;
+                load(sV + b * MSK_KV, &tv, &sh.v_full[b], B0 + n);
+                nv = n + 1;
             }
             // No copy may still be landing when the CTA exits, also when a wait ran out.
             if (lane == 0) {
-                for (int m = n > 2 ? n - 2 : 0; m < n; m++) drain_wait(&full[m & 1], (m >> 1) & 1);
+                auto drain = [&](uint64_t* full, int issued) {
+                    for (int m = issued > MSK_SLOTS ? issued - MSK_SLOTS : 0; m < issued; m++)
+                        drain_wait(&full[m % MSK_SLOTS], (m / MSK_SLOTS) & 1);
+                };
+                drain(sh.k_full, nk);
+                drain(sh.v_full, nv);
                 for (int x = 0; x < nq; x++) drain_wait(&sh.q_full[x], 0);
             }
             __syncwarp();
         } else if (warp == MSK_GATE_WARP) {
             // ------------------------------------------------------------ V's gate
             for (int n = 0; n < B1 - B0; n++) {
-                const int b = n & 1;
-                if (!__all_sync(~0u, att_wait(&sh.v_full[b], (n >> 1) & 1))) break;
+                const int b = n % MSK_SLOTS;
+                if (!__all_sync(~0u, att_wait(&sh.v_full[b], (n / MSK_SLOTS) & 1))) break;
                 if (!whole(B0 + n)) {
-                    if (lane < 4) sh.flags[b][lane] = 0;
+                    if (lane < 2) sh.flags[b][lane] = 0;
                     __syncwarp();
-                    uint4* const v = reinterpret_cast<uint4*>(sV + b * ATT_TILE);
+                    uint4* const v = reinterpret_cast<uint4*>(sV + b * MSK_KV);
                     // an f16 with all exponent bits set carries into its sign bit
                     auto c = [](uint32_t y) { return (y & 0x7fff7fffu) + 0x04000400u; };
 #pragma unroll 1
-                    for (int i0 = lane; i0 < ATT_TILE / 16; i0 += 8 * 32) {
+                    for (int i0 = lane; i0 < MSK_KV / 16; i0 += 8 * 32) {
                         uint4 x[8];
 #pragma unroll
                         for (int e = 0; e < 8; e++) x[e] = v[i0 + 32 * e];
@@ -241,7 +286,7 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
                             };
                             if (!((c(y.x) | c(y.y) | c(y.z) | c(y.w)) & 0x80008000u)) continue;
                             v[i] = make_uint4(z(y.x), z(y.y), z(y.z), z(y.w));
-                            const int key = (i >> 3) & 127;  // 128-byte rows of 64 head-dim values
+                            const int key = (i >> 3) & (MSK_BK - 1);  // 128-byte rows of 64 head-dim values
                             atomicOr(&sh.flags[b][key >> 5], 1u << (key & 31));
                         }
                     }
@@ -250,64 +295,72 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
                 }
                 if (lane == 0) mbar_arrive(&sh.v_ready[b]);
             }
-        } else if (lane == 0) {
-            // ------------------------------------------------------------ MMA issue
+        } else {
+            // ------------------------------------------------------------ MMA issue, tile x
             constexpr uint32_t ID_S = idesc_f16(128, MSK_BK);
             constexpr uint32_t ID_O = idesc_f16(128, ATT_DH) | (1u << 16);  // B (V) MN-major
-            const uint64_t dq = att_qk_desc(sQ), dk = att_qk_desc(sK), dv = att_v_desc(sV);
+            const int x = __shfl_sync(~0u, warp - MSK_MMA_WARP, 0);
+            const uint32_t el = elect_one();
+            const uint32_t tO = tm + 256 * x, tS = tO + 128;
+            const uint64_t dq = att_qk_desc(sQ) + (uint64_t)(x * (ATT_TILE >> 4)), dk = att_qk_desc(sK);
+            const uint64_t dv = sdesc_sw128(smem_u32(sV), MSK_KV / 2, 1024);
+            const int kb0 = x ? t0[1] : t0[0], kb1 = x ? t1[1] : t1[0];
             bool ok = true;
-            // One step beyond the last block: its P V only.
-            for (int n = 0; ok && n <= B1 - B0; n++) {
-                const int kb = B0 + n, b = n & 1;
+            auto wait = [&](uint64_t* bar, uint32_t parity) { ok = ok && __all_sync(~0u, att_wait(bar, parity)); };
+            // S(kb) of the n-th block.  A block outside the tile's range is waited for all the
+            // same before its slot is given back.
+            auto scores = [&](int n) {
+                const int kb = B0 + n, b = n % MSK_SLOTS, sl = (kb - kb0) & 1;
+                if (kb >= B1) return;
+                wait(&sh.k_full[b], (n / MSK_SLOTS) & 1);
+                if (!ok) return;
+                if (kb >= kb0 && kb < kb1) {
+                    tc_fence_after();
+                    const uint64_t d = dk + (uint64_t)(b * (MSK_KV >> 4));
+                    const uint32_t ts = tS + 64 * sl;
+                    mma_f16_ss_if(el, ts, dq, d, ID_S, 0);
 #pragma unroll
-                for (int x = 0; x < 2; x++) {
-                    const uint32_t tO = tm + 256 * x, tS = tO + 128;
-                    if (ok && n > 0 && kb - 1 >= t0[x] && kb - 1 < t1[x]) {
-                        const int p = b ^ 1;  // slot of block kb - 1
-                        ok = ok && att_wait(&sh.p_full[x], (kb - 1 - t0[x]) & 1) && att_wait(&sh.v_ready[p], ((n - 1) >> 1) & 1);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint64_t d = dv + (uint64_t)(p * (ATT_TILE >> 4));
-                        mma_f16_ts(tO, tS, d, ID_O, kb - 1 > t0[x]);
+                    for (int kk = 1; kk < ATT_DH / 16; kk++)
+                        mma_f16_ss_if(el, ts, dq + att_qk_step(kk), d + att_k64_step(kk), ID_S, 1);
+                    if (el) tc_commit(&sh.s_full[x][sl]);
+                }
+                if (el) tc_commit(&sh.k_empty[b]);
+            };
+            if (kb0 < kb1) wait(&sh.q_full[x], 0);
+            if (ok) scores(0);
+            if (ok) scores(1);
+            for (int n = 0; ok && n < B1 - B0; n++) {
+                const int kb = B0 + n, b = n % MSK_SLOTS, sl = (kb - kb0) & 1;
+                wait(&sh.v_ready[b], (n / MSK_SLOTS) & 1);
+                if (kb >= kb0 && kb < kb1) {
+                    wait(&sh.p_full[x][sl], ((kb - kb0) >> 1) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t d = dv + (uint64_t)(b * (MSK_KV >> 4));
+                    const uint32_t tp = tS + 64 * sl;
+                    mma_f16_ts_if(el, tO, tp, d, ID_O, kb > kb0);
 #pragma unroll
-                        for (int kk = 1; kk < MSK_BK / 16; kk++) mma_f16_ts(tO, tS + 8 * kk, d + att_v_step(kk), ID_O, 1);
-                        if (kb == t1[x]) tc_commit(&sh.o_done[x]);
-                    }
-                    if (ok && kb >= t0[x] && kb < t1[x]) {
-                        ok = (kb > t0[x] || att_wait(&sh.q_full[x], 0)) && att_wait(&sh.k_full[b], (n >> 1) & 1);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint64_t q = dq + (uint64_t)(x * (ATT_TILE >> 4)), d = dk + (uint64_t)(b * (ATT_TILE >> 4));
-                        mma_f16_ss(tS, q, d, ID_S, 0);
-#pragma unroll
-                        for (int kk = 1; kk < ATT_DH / 16; kk++)
-                            mma_f16_ss(tS, q + att_qk_step(kk), d + att_qk_step(kk), ID_S, 1);
-                        tc_commit(&sh.s_full[x]);
-                    }
+                    for (int kk = 1; kk < MSK_BK / 16; kk++)
+                        mma_f16_ts_if(el, tO, tp + 8 * kk, d + att_v_step(kk), ID_O, 1);
+                    if (el) tc_commit(&sh.o_done[x][sl]);
                 }
-                if (ok && n > 0) {
-                    // a block that no tile multiplied still passes its gate before its slot is refilled
-                    ok = att_wait(&sh.v_ready[b ^ 1], ((n - 1) >> 1) & 1);
-                    tc_commit(&sh.v_empty[b ^ 1]);
-                }
-                if (ok && kb < B1) {
-                    ok = att_wait(&sh.k_full[b], (n >> 1) & 1);
-                    tc_commit(&sh.k_empty[b]);
-                }
+                if (!ok) break;
+                if (el) tc_commit(&sh.v_empty[b]);
+                scores(n + 2);
             }
             // Every MMA issued above completes before tensor memory is released.
-            tc_commit(&sh.fin);
-            drain_wait(&sh.fin, 0);
+            if (el) {
+                tc_commit(&sh.fin);
+                drain_wait(&sh.fin, 0);
+            }
         }
         __syncwarp();
     } else {
         // ---------------------------------------------------------------- softmax, output
         setmaxnreg_inc<MSK_REG_SOFTMAX>();
-        const uint32_t tl = tm + ((uint32_t)(32 * quad) << 16) + 256 * t;
-        const uint32_t tO = tl + 64 * half, tS = tl + 128 + 64 * half, tP = tl + 128 + 32 * half;
+        const uint32_t tO = tm + ((uint32_t)(32 * quad) << 16) + 256 * t;
         const int kb0 = t ? t0[1] : t0[0], kb1 = t ? t1[1] : t1[0];
-        const int sw = 4 * t + quad, bar = 1 + sw;
-        const int w_lo0 = sh.lo_min[sw], w_hi1 = sh.hi_max[sw], w_lo1 = sh.lo_max[sw], w_hi0 = sh.hi_min[sw];
+        const int w_lo0 = sh.lo_min[warp], w_hi1 = sh.hi_max[warp], w_lo1 = sh.lo_max[warp], w_hi0 = sh.hi_min[warp];
         const bool some = lo < hi;
         if (!some) lo = 0, hi = a.Lk;  // a row without keys runs along; it stores zeros
         float slope = 0.0f;
@@ -317,71 +370,64 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
             qp = a.q_pos ? __ldg(a.q_pos + qi) : qi + a.Lk - a.Lq;
         }
         float m = -INFINITY, l = 0.0f;
-        bool ok = true;  // alike in the two warps of a row after every barrier of theirs
+        bool ok = true;
         for (int kb = kb0; kb < kb1; kb++) {
-            ok = __all_sync(~0u, att_wait(&sh.s_full[t], (kb - kb0) & 1));
-            if (ok) tc_fence_after();
-            const int k0 = kb * MSK_BK + 64 * half;  // this half's first key
-            if (kb * MSK_BK >= w_hi1 || (kb + 1) * MSK_BK <= w_lo0) {  // no row of the two warps sees the block
-                ok = named_barrier_and(bar, 64, ok);  // the two warps stop together or not at all
-                if (!ok) break;
+            const int sl = (kb - kb0) & 1, use = (kb - kb0) >> 1, k0 = kb * MSK_BK;
+            const uint32_t tS = tO + 128 + 64 * sl;
+            ok = __all_sync(~0u, att_wait(&sh.s_full[t][sl], use & 1));
+            if (!ok) break;
+            tc_fence_after();
+            const bool unseen = k0 >= w_hi1 || k0 + MSK_BK <= w_lo0;  // by any row of the warp
+            if (unseen) {
                 uint32_t z[16];
 #pragma unroll
                 for (int e = 0; e < 16; e++) z[e] = 0u;
-                tmem_st16(tP, z);
-                tmem_st16(tP + 16, z);
+                tmem_st16(tS, z);
+                tmem_st16(tS + 16, z);
             } else {
-                float s[64];
-                if (ok) {
+                float s[MSK_BK];
 #pragma unroll
-                    for (int c = 0; c < 4; c++) tmem_ld16(tS + 16 * c, reinterpret_cast<uint32_t*>(s) + 16 * c);
-                    tmem_wait_ld();
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 64; j++) s[j] = 0.0f;
-                }
+                for (int c = 0; c < 4; c++) tmem_ld16(tS + 16 * c, reinterpret_cast<uint32_t*>(s) + 16 * c);
+                tmem_wait_ld();
                 if constexpr (CAP) {
 #pragma unroll
-                    for (int j = 0; j < 64; j++) s[j] = a.cap_out * att_tanh(s[j] * a.cap_in);
+                    for (int j = 0; j < MSK_BK; j++) s[j] = a.cap_out * att_tanh(s[j] * a.cap_in);
                 } else if constexpr (BIAS) {
 #pragma unroll
-                    for (int j = 0; j < 64; j++) s[j] *= ATT_C;
+                    for (int j = 0; j < MSK_BK; j++) s[j] *= ATT_C;
                 }
                 if constexpr (BIAS) {
                     const float d = (float)((int64_t)qp - k0);
 #pragma unroll
-                    for (int j = 0; j < 64; j++) s[j] = fmaf(-slope, fabsf(d - (float)j), s[j]);
+                    for (int j = 0; j < MSK_BK; j++) s[j] = fmaf(-slope, fabsf(d - (float)j), s[j]);
                 }
-                if (k0 < w_lo1 || k0 + 64 > w_hi0) {  // warp-uniform: some row hides some key
+                if (k0 < w_lo1 || k0 + MSK_BK > w_hi0) {  // warp-uniform: some row hides some key
                     const int from = lo - k0, n = hi - lo;
 #pragma unroll
-                    for (int j = 0; j < 64; j++)
+                    for (int j = 0; j < MSK_BK; j++)
                         if ((uint32_t)(j - from) >= (uint32_t)n) s[j] = -INFINITY;
                 }
                 float mx[4];
 #pragma unroll
                 for (int e = 0; e < 4; e++) mx[e] = fmaxf(s[e], s[4 + e]);
 #pragma unroll
-                for (int j = 8; j < 64; j += 8)
+                for (int j = 8; j < MSK_BK; j += 8)
 #pragma unroll
                     for (int e = 0; e < 4; e++) mx[e] = max3f(mx[e], s[j + e], s[j + 4 + e]);
                 constexpr float C = CAP || BIAS ? 1.0f : ATT_C;
-                float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * C;
-                // Both warps have S in registers after this barrier: P may be written over it.
-                const bool calm = named_barrier_and(bar, 64, ok && !(top > m + ATT_RESCALE_LOG2));
-                if (!calm) {
-                    sh.swap[t][half][row] = top;
-                    ok = named_barrier_and(bar, 64, ok);
-                    if (!ok) break;
-                    top = fmaxf(top, sh.swap[t][half ^ 1][row]);
-                    const bool raise = top > m + ATT_RESCALE_LOG2;  // also from -inf; not where all is hidden
-                    // S(kb) is committed after P V(kb - 1): O is complete
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * C;
+                const bool raise = top > m + ATT_RESCALE_LOG2;  // also from -inf; not where all is hidden
+                if (__any_sync(~0u, raise)) {
                     const float alpha = raise ? att_ex2(m - top) : 1.0f;  // 0 from -inf
                     if (raise) m = top;
                     l *= alpha;
                     if (kb > kb0) {
+                        // O must hold the blocks before this one
+                        ok = __all_sync(~0u, att_wait(&sh.o_done[t][sl ^ 1], ((kb - 1 - kb0) >> 1) & 1));
+                        if (!ok) break;
+                        tc_fence_after();
 #pragma unroll 1
-                        for (int c = 0; c < 4; c++) {
+                        for (int c = 0; c < 8; c++) {
                             uint32_t r[16];
                             tmem_ld16(tO + 16 * c, r);
                             tmem_wait_ld();
@@ -407,41 +453,36 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
                         sum[e & 1] = fadd2(sum[e & 1], x);
                         pk[e] = pack_h2(x.x, x.y);
                     }
-                    tmem_st16(tP + 16 * c, pk);
+                    tmem_st16(tS + 16 * c, pk);
                 }
                 const float2 u = fadd2(sum[0], sum[1]);
                 l += u.x + u.y;
             }
+            if (!unseen && !whole(kb)) {  // V's gate: a marked key of the row's own?
+                // (before P is handed over: after that the slot may be refilled)
+                const int n = kb - B0, b = n % MSK_SLOTS;
+                if (!__all_sync(~0u, att_wait(&sh.v_ready[b], (n / MSK_SLOTS) & 1))) l = NAN;
+#pragma unroll 1
+                for (int w = 0; w < 2; w++)
+                    for (uint32_t f = sh.flags[b][w]; f; f &= f - 1)
+                        if ((uint32_t)(k0 + 32 * w + __ffs(f) - 1 - lo) < (uint32_t)(hi - lo)) l = NAN;
+            }
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.p_full[t]);
-            if (!whole(kb) && !(kb * MSK_BK >= w_hi1 || (kb + 1) * MSK_BK <= w_lo0)) {
-                // the gate has looked at V: a marked key of the row's own?
-                const int b = (kb - B0) & 1;
-                if (!__all_sync(~0u, att_wait(&sh.v_ready[b], ((kb - B0) >> 1) & 1))) l = NAN;
-#pragma unroll 1
-                for (int w = 2 * half; w < 2 * half + 2; w++)
-                    for (uint32_t f = sh.flags[b][w]; f; f &= f - 1)
-                        if ((uint32_t)(kb * MSK_BK + 32 * w + __ffs(f) - 1 - lo) < (uint32_t)(hi - lo)) l = NAN;
-            }
+            if (lane == 0) mbar_arrive(&sh.p_full[t][sl]);
         }
         const bool ran = kb0 < kb1;
-        if (ran && ok) ok = __all_sync(~0u, att_wait(&sh.o_done[t], 0));
-        if (ran) {
-            sh.swap[t][half][row] = l;
-            ok = named_barrier_and(bar, 64, ok);
-            l += sh.swap[t][half ^ 1][row];
-        }
+        if (ran && ok) ok = __all_sync(~0u, att_wait(&sh.o_done[t][(kb1 - 1 - kb0) & 1], ((kb1 - 1 - kb0) >> 1) & 1));
         if (ok) {
             tc_fence_after();
             const int64_t at = (int64_t)qi * a.H + head;
             const bool split = a.splits > 1;
             const int64_t pat = (int64_t)blockIdx.y * a.Lq * a.H + at;
             const float inv = some && ran ? (split ? 1.0f : 1.0f / l) : 0.0f;
-            if (split && live && half == 0) a.part_ml[pat] = some && ran ? make_float2(m, l) : make_float2(-INFINITY, 0.0f);
-#pragma unroll
-            for (int c = 0; c < 2; c++) {
+            if (split && live) a.part_ml[pat] = some && ran ? make_float2(m, l) : make_float2(-INFINITY, 0.0f);
+#pragma unroll 1
+            for (int c = 0; c < 4; c++) {
                 float r[32];
                 if (ran) {
                     tmem_ld16(tO + 32 * c, reinterpret_cast<uint32_t*>(r));
@@ -451,14 +492,13 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
 #pragma unroll
                 for (int e = 0; e < 32; e++) r[e] = some && ran ? r[e] * inv : 0.0f;
                 if (!live || (split && !ran)) continue;
-                const int64_t col = 64 * half + 32 * c;
                 if (split || !a.o_f16) {
-                    float* dst = (split ? a.part + pat * ATT_DH : static_cast<float*>(a.o) + at * ATT_DH) + col;
+                    float* dst = (split ? a.part + pat * ATT_DH : static_cast<float*>(a.o) + at * ATT_DH) + 32 * c;
 #pragma unroll
                     for (int e = 0; e < 8; e++)
                         reinterpret_cast<float4*>(dst)[e] = make_float4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
                 } else {
-                    __half* dst = static_cast<__half*>(a.o) + at * ATT_DH + col;
+                    __half* dst = static_cast<__half*>(a.o) + at * ATT_DH + 32 * c;
 #pragma unroll
                     for (int e = 0; e < 4; e++)
                         reinterpret_cast<uint4*>(dst)[e] =

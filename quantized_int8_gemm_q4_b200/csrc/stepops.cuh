@@ -50,7 +50,7 @@ struct MaskPlan {
 
 // Tiles, CTAs and key parts of a masked attention call.  Two query tiles per CTA once one
 // each would need more than one wave; with at most half a wave of CTAs the keys are cut
-// into parts of at least two blocks, up to one wave in all.
+// into parts of at least four blocks, up to one wave in all.
 MaskPlan mask_plan(int64_t Lq, int64_t Lk, int64_t H, int64_t Hkv, int sms) {
     MaskPlan p;
     const int group = (int)(H / Hkv);
@@ -61,9 +61,9 @@ MaskPlan mask_plan(int64_t Lq, int64_t Lk, int64_t H, int64_t Hkv, int sms) {
     p.tiles = n_tiles * n_heads > sms ? 2 : 1;
     p.grid = (n_tiles + p.tiles - 1) / p.tiles * n_heads;
     p.splits = 1;
-    if (2 * p.grid <= sms && blocks >= 4) {
+    if (2 * p.grid <= sms && blocks >= 8) {
         const int64_t most = sms / p.grid;
-        p.splits = (int)(most < blocks / 2 ? most : blocks / 2);
+        p.splits = (int)(most < blocks / 4 ? most : blocks / 4);
     }
     p.ml_off = p.bytes = 0;
     if (p.splits > 1) {
