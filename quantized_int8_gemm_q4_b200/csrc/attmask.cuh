@@ -90,6 +90,9 @@ __device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
     return *reinterpret_cast<float2*>(&d);
 }
 
+__device__ __forceinline__ void prefetch_tensormap(const void* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
 // One lane of a converged warp, as a predicate.
 __device__ __forceinline__ uint32_t elect_one() {
     uint32_t r;
@@ -146,7 +149,14 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
     const int q0 = (int)((gridDim.x - 1 - blockIdx.x) / n_heads) * a.tiles * a.tq;
     const int ntiles = a.tiles == 2 && a.Lq - q0 > a.tq ? 2 : 1;
 
-    if (threadIdx.x == 32 * MSK_MMA_WARP) {
+    if (warp == MSK_MMA_WARP) {
+        tmem_alloc(&sh.tmem, ATT_TM_COLS);
+        tmem_relinquish();
+    }
+    if (threadIdx.x == 32 * MSK_TMA_WARP) {
+        prefetch_tensormap(&tq);
+        prefetch_tensormap(&tk);
+        prefetch_tensormap(&tv);
         for (int b = 0; b < 2; b++) {
             mbar_init(&sh.q_full[b], 1);
             for (int x = 0; x < 2; x++) {
@@ -165,13 +175,17 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
         mbar_init(&sh.fin, 2);
         fence_mbar_init();
     }
-    if (warp == MSK_MMA_WARP) {
-        __syncwarp();
-        tmem_alloc(&sh.tmem, ATT_TM_COLS);
-        tmem_relinquish();
-    }
     pdl_trigger();
     pdl_wait();  // q, k, v and the intervals may come from the previous kernel on the stream
+    if (warp == MSK_TMA_WARP) {
+        // the queries at once, while the intervals are read
+        __syncwarp();
+        for (int x = 0; x < ntiles; x++) {
+            if (lane == 0) mbar_arrive_expect_tx(&sh.q_full[x], (uint32_t)(a.gp * a.tq) * ATT_DH * 2);
+            __syncwarp();
+            att_tma_tile(sQ + x * ATT_TILE, &tq, h0, q0 + x * a.tq, &sh.q_full[x], lane);
+        }
+    }
 
     // This thread's row (softmax warps): query, head, interval.
     const int t = warp >> 2, quad = warp & 3, row = threadIdx.x & 127;
@@ -225,12 +239,6 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
         setmaxnreg_dec<MSK_REG_OTHER>();
         if (warp == MSK_TMA_WARP) {
             // ------------------------------------------------------------ TMA producer
-            const int nq = B0 < B1 ? ntiles : 0;
-            for (int x = 0; x < nq; x++) {
-                if (lane == 0) mbar_arrive_expect_tx(&sh.q_full[x], (uint32_t)(a.gp * a.tq) * ATT_DH * 2);
-                __syncwarp();
-                att_tma_tile(sQ + x * ATT_TILE, &tq, h0, q0 + x * a.tq, &sh.q_full[x], lane);
-            }
             int nk = 0, nv = 0;
             auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* full, int kb) {
                 if (lane == 0) mbar_arrive_expect_tx(full, MSK_KV);
@@ -255,7 +263,7 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
                 };
                 drain(sh.k_full, nk);
                 drain(sh.v_full, nv);
-                for (int x = 0; x < nq; x++) drain_wait(&sh.q_full[x], 0);
+                for (int x = 0; x < ntiles; x++) drain_wait(&sh.q_full[x], 0);
             }
             __syncwarp();
         } else if (warp == MSK_GATE_WARP) {
@@ -474,6 +482,8 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
         }
         const bool ran = kb0 < kb1;
         if (ran && ok) ok = __all_sync(~0u, att_wait(&sh.o_done[t][(kb1 - 1 - kb0) & 1], ((kb1 - 1 - kb0) >> 1) & 1));
+        // a tile without a block: its queries' copy must have landed before the space is used again
+        if (!ran && t < ntiles) ok = __all_sync(~0u, att_wait(&sh.q_full[t], 0));
         if (ok) {
             tc_fence_after();
             const int64_t at = (int64_t)qi * a.H + head;
@@ -481,30 +491,52 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
             const int64_t pat = (int64_t)blockIdx.y * a.Lq * a.H + at;
             const float inv = some && ran ? (split ? 1.0f : 1.0f / l) : 0.0f;
             if (split && live) a.part_ml[pat] = some && ran ? make_float2(m, l) : make_float2(-INFINITY, 0.0f);
+            // O through shared memory (this warp's 8 KB of its tile's queries, which no MMA
+            // reads any more), so that a store covers two whole rows of 256 bytes: 32 rows of
+            // 16 bytes keep the store unit busy for 32 cycles (4000 in all for a CTA).  Rows
+            // of 16 chunks, chunk c of row i at c ^ (i & 15).
+            const bool f32 = split || !a.o_f16;
+            uint8_t* const buf = sQ + t * ATT_TILE + quad * 8192;
+            const int64_t mine = live && !(split && !ran) ? (split ? pat : at) : -1;
 #pragma unroll 1
-            for (int c = 0; c < 4; c++) {
-                float r[32];
-                if (ran) {
-                    tmem_ld16(tO + 32 * c, reinterpret_cast<uint32_t*>(r));
-                    tmem_ld16(tO + 32 * c + 16, reinterpret_cast<uint32_t*>(r) + 16);
-                    tmem_wait_ld();
+            for (int c = 0; c < (f32 ? 2 : 1); c++) {  // f32: 64 columns at a time
+#pragma unroll 1
+                for (int d = 0; d < (f32 ? 2 : 4); d++) {
+                    float r[32];
+                    if (ran) {
+                        tmem_ld16(tO + 64 * c + 32 * d, reinterpret_cast<uint32_t*>(r));
+                        tmem_ld16(tO + 64 * c + 32 * d + 16, reinterpret_cast<uint32_t*>(r) + 16);
+                        tmem_wait_ld();
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; e++) r[e] = some && ran ? r[e] * inv : 0.0f;
+                    auto put = [&](int chunk, uint4 x) {
+                        *reinterpret_cast<uint4*>(buf + lane * 256 + ((chunk ^ (lane & 15)) * 16)) = x;
+                    };
+                    if (f32) {
+#pragma unroll
+                        for (int e = 0; e < 8; e++)
+                            put(8 * d + e, make_uint4(__float_as_uint(r[4 * e]), __float_as_uint(r[4 * e + 1]),
+                                                      __float_as_uint(r[4 * e + 2]), __float_as_uint(r[4 * e + 3])));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; e++)
+                            put(4 * d + e, make_uint4(pack_h2(r[8 * e], r[8 * e + 1]), pack_h2(r[8 * e + 2], r[8 * e + 3]),
+                                                      pack_h2(r[8 * e + 4], r[8 * e + 5]), pack_h2(r[8 * e + 6], r[8 * e + 7])));
+                    }
                 }
-#pragma unroll
-                for (int e = 0; e < 32; e++) r[e] = some && ran ? r[e] * inv : 0.0f;
-                if (!live || (split && !ran)) continue;
-                if (split || !a.o_f16) {
-                    float* dst = (split ? a.part + pat * ATT_DH : static_cast<float*>(a.o) + at * ATT_DH) + 32 * c;
-#pragma unroll
-                    for (int e = 0; e < 8; e++)
-                        reinterpret_cast<float4*>(dst)[e] = make_float4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
-                } else {
-                    __half* dst = static_cast<__half*>(a.o) + at * ATT_DH + 32 * c;
-#pragma unroll
-                    for (int e = 0; e < 4; e++)
-                        reinterpret_cast<uint4*>(dst)[e] =
-                            make_uint4(pack_h2(r[8 * e], r[8 * e + 1]), pack_h2(r[8 * e + 2], r[8 * e + 3]),
-                                       pack_h2(r[8 * e + 4], r[8 * e + 5]), pack_h2(r[8 * e + 6], r[8 * e + 7]));
+                __syncwarp();
+                uint8_t* const out = static_cast<uint8_t*>(split ? static_cast<void*>(a.part) : a.o);
+                const int row_bytes = f32 ? 512 : 256;
+#pragma unroll 4
+                for (int i = 0; i < 16; i++) {
+                    const int rw = 2 * i + (lane >> 4), chunk = lane & 15;
+                    const int64_t to = __shfl_sync(~0u, mine, rw);
+                    if (to < 0) continue;
+                    *reinterpret_cast<uint4*>(out + to * row_bytes + 256 * c + chunk * 16) =
+                        *reinterpret_cast<const uint4*>(buf + rw * 256 + ((chunk ^ (rw & 15)) * 16));
                 }
+                __syncwarp();
             }
         }
     }
