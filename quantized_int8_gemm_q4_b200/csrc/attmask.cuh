@@ -500,35 +500,35 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
             const int64_t mine = live && !(split && !ran) ? (split ? pat : at) : -1;
 #pragma unroll 1
             for (int c = 0; c < (f32 ? 2 : 1); c++) {  // f32: 64 columns at a time
+// (small loops: this code runs once per CTA, so its time is that of fetching it)
 #pragma unroll 1
-                for (int d = 0; d < (f32 ? 2 : 4); d++) {
-                    float r[32];
+                for (int d = 0; d < (f32 ? 4 : 8); d++) {
+                    float r[16];
                     if (ran) {
-                        tmem_ld16(tO + 64 * c + 32 * d, reinterpret_cast<uint32_t*>(r));
-                        tmem_ld16(tO + 64 * c + 32 * d + 16, reinterpret_cast<uint32_t*>(r) + 16);
+                        tmem_ld16(tO + 64 * c + 16 * d, reinterpret_cast<uint32_t*>(r));
                         tmem_wait_ld();
                     }
 #pragma unroll
-                    for (int e = 0; e < 32; e++) r[e] = some && ran ? r[e] * inv : 0.0f;
+                    for (int e = 0; e < 16; e++) r[e] = some && ran ? r[e] * inv : 0.0f;
                     auto put = [&](int chunk, uint4 x) {
                         *reinterpret_cast<uint4*>(buf + lane * 256 + ((chunk ^ (lane & 15)) * 16)) = x;
                     };
                     if (f32) {
 #pragma unroll
-                        for (int e = 0; e < 8; e++)
-                            put(8 * d + e, make_uint4(__float_as_uint(r[4 * e]), __float_as_uint(r[4 * e + 1]),
+                        for (int e = 0; e < 4; e++)
+                            put(4 * d + e, make_uint4(__float_as_uint(r[4 * e]), __float_as_uint(r[4 * e + 1]),
                                                       __float_as_uint(r[4 * e + 2]), __float_as_uint(r[4 * e + 3])));
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 4; e++)
-                            put(4 * d + e, make_uint4(pack_h2(r[8 * e], r[8 * e + 1]), pack_h2(r[8 * e + 2], r[8 * e + 3]),
+                        for (int e = 0; e < 2; e++)
+                            put(2 * d + e, make_uint4(pack_h2(r[8 * e], r[8 * e + 1]), pack_h2(r[8 * e + 2], r[8 * e + 3]),
                                                       pack_h2(r[8 * e + 4], r[8 * e + 5]), pack_h2(r[8 * e + 6], r[8 * e + 7])));
                     }
                 }
                 __syncwarp();
                 uint8_t* const out = static_cast<uint8_t*>(split ? static_cast<void*>(a.part) : a.o);
                 const int row_bytes = f32 ? 512 : 256;
-#pragma unroll 4
+#pragma unroll 2
                 for (int i = 0; i < 16; i++) {
                     const int rw = 2 * i + (lane >> 4), chunk = lane & 15;
                     const int64_t to = __shfl_sync(~0u, mine, rw);
