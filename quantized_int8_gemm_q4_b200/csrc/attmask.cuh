@@ -10,8 +10,10 @@
 // (the largest divisor of the group up to 128) x 128 / gp queries, row = query * gp + head,
 // which is the order in which one TMA box of gp heads x 128 / gp rows lands in shared memory.  So
 // grouped heads read their keys once, and one query of 8 heads fills 8 rows.  A CTA has two
-// tiles (one for small grids) and the key blocks of 64 that any of their rows sees, or one of
-// `splits` equal parts of them; 12 warps:
+// tiles and the key blocks of 64 that any of their rows sees, or one of `splits` equal parts
+// of them.  In grids of less than a wave its two tiles are the same queries ("halves"): the
+// first takes the first half of the blocks, the second the others, and their results are
+// joined from tensor memory at the end, so that two chains of blocks run on each SM.  12 warps:
 //   warps 0-3, 4-7  softmax of tile 0, tile 1; thread = row, all 64 scores of a block in
 //                   registers; the running maximum is raised by more than 2^8 at a time
 //   warp 8, 9       issue the MMAs of tile 0, tile 1 (S = Q K^T, O += P V; kind::f16, f32 in
@@ -44,7 +46,10 @@ constexpr int MSK_SOFTMAX_WARPS = 8;
 constexpr int MSK_MMA_WARP = 8, MSK_TMA_WARP = 10, MSK_GATE_WARP = 11;  // 8, 9: one per tile
 constexpr int MSK_THREADS = 32 * 12;
 constexpr int MSK_BK = 64;    // keys per block
-constexpr int MSK_SLOTS = 4;  // K and V slots
+constexpr int MSK_SLOTS = 4;    // K slots, and V slots of two query tiles
+// Halves have one query tile, whose pair's space goes to V: with the scores of four blocks
+// ahead four V blocks wait for their weights, and as many are on their way.
+constexpr int MSK_V_SLOTS = 8;
 constexpr int MSK_KV = MSK_BK * ATT_DH * 2;
 // Registers per thread after setmaxnreg (softmax warpgroups; the others), out of the
 // launch's 384 x 168.
@@ -52,18 +57,20 @@ constexpr int MSK_REG_SOFTMAX = 200, MSK_REG_OTHER = 96, MSK_REG_LAUNCH = 168;
 static_assert(256 * MSK_REG_SOFTMAX + 128 * MSK_REG_OTHER <= MSK_THREADS * MSK_REG_LAUNCH, "setmaxnreg split");
 
 struct MaskShared {
-    uint64_t q_full[2], k_full[MSK_SLOTS], v_full[MSK_SLOTS], v_ready[MSK_SLOTS], k_empty[MSK_SLOTS], v_empty[MSK_SLOTS];
+    uint64_t q_full[2], k_full[MSK_SLOTS], k_empty[MSK_SLOTS];
+    uint64_t v_full[MSK_V_SLOTS], v_ready[MSK_V_SLOTS], v_empty[MSK_V_SLOTS];
     uint64_t s_full[2][2], p_full[2][2], o_done[2][2], fin;  // [tile][S slot]
-    uint32_t tmem, flags[MSK_SLOTS][2];  // per V slot, bit j: key j's value is not finite
+    uint32_t tmem, flags[MSK_V_SLOTS][2];  // per V slot, bit j: key j's value is not finite
     int32_t lo_min[8], hi_max[8], lo_max[8], hi_min[8];  // per softmax warp, over rows with keys
+    float2 ml[2][128];  // halves: each row's maximum and sum
 };
-// Q x2, K x4, V x4, barriers
-constexpr size_t MSK_SMEM = 2 * (size_t)ATT_TILE + 2 * MSK_SLOTS * (size_t)MSK_KV + sizeof(MaskShared);
+// Q x2, K x4, V x4 or Q, K x4, V x8; barriers
+constexpr size_t msk_smem(bool halves) { return (halves ? 7 : 6) * (size_t)ATT_TILE + sizeof(MaskShared); }
+static_assert(msk_smem(true) <= 227 * 1024, "shared memory of a CTA");
 
 struct MaskArgs {
     int32_t Lq, Lk, H, group;
     int32_t gp, tq;   // heads and queries per tile
-    int32_t tiles;    // query tiles per CTA (1 or 2)
     int32_t splits;   // parts of the key range (grid y)
     const int32_t *kv_begin, *kv_end, *q_pos;
     float cap_in, cap_out;  // s' = cap_out tanh(cap_in qk), in base-2 exponents
@@ -131,23 +138,27 @@ __device__ __forceinline__ float att_tanh(float y) {
     return 1.0f - __fdividef(2.0f, 1.0f + e);
 }
 
-// MODE bit 0: cap, bit 1: distance bias.
+// MODE bit 0: cap, bit 1: distance bias, bit 2: halves.
 template <int MODE>
 __global__ void __launch_bounds__(MSK_THREADS, 1)
     attention_masked_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                             const __grid_constant__ CUtensorMap tv, const __grid_constant__ MaskArgs a) {
-    constexpr bool CAP = MODE & 1, BIAS = MODE & 2;
+    constexpr bool CAP = MODE & 1, BIAS = MODE & 2, halves = MODE & 4;
     extern __shared__ __align__(1024) uint8_t smem[];
-    uint8_t* const sQ = smem;                       // two tiles
-    uint8_t* const sK = smem + 2 * ATT_TILE;        // four slots
-    uint8_t* const sV = sK + MSK_SLOTS * MSK_KV;    // four slots
-    MaskShared& sh = *reinterpret_cast<MaskShared*>(sV + MSK_SLOTS * MSK_KV);
+    uint8_t* const sQ = smem;                                   // one or two tiles
+    uint8_t* const sK = smem + (halves ? 1 : 2) * ATT_TILE;     // four slots
+    uint8_t* const sV = sK + MSK_SLOTS * MSK_KV;                // v_slots slots
+    constexpr int v_log = halves ? 3 : 2, v_slots = 1 << v_log;
+    MaskShared& sh = *reinterpret_cast<MaskShared*>(sV + v_slots * MSK_KV);
+    // Slot and parity of V block n.
+    auto v_slot = [&](int n) { return n & (v_slots - 1); };
+    auto v_use = [&](int n) { return (uint32_t)(n >> v_log) & 1; };
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // The last queries first (under causal intervals theirs are the longest), all heads of them.
     const int n_heads = a.H / a.gp, h0 = (int)(blockIdx.x % n_heads) * a.gp, hk = h0 / a.group;
-    const int q0 = (int)((gridDim.x - 1 - blockIdx.x) / n_heads) * a.tiles * a.tq;
-    const int ntiles = a.tiles == 2 && a.Lq - q0 > a.tq ? 2 : 1;
+    const int q0 = (int)((gridDim.x - 1 - blockIdx.x) / n_heads) * (halves ? 1 : 2) * a.tq;
+    const int ntiles = !halves && a.Lq - q0 > a.tq ? 2 : 1;  // with queries of their own
 
     if (warp == MSK_MMA_WARP) {
         tmem_alloc(&sh.tmem, ATT_TM_COLS);
@@ -167,9 +178,11 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
         }
         for (int b = 0; b < MSK_SLOTS; b++) {
             mbar_init(&sh.k_full[b], 1);
+            mbar_init(&sh.k_empty[b], 2);  // both tiles' issuers
+        }
+        for (int b = 0; b < MSK_V_SLOTS; b++) {
             mbar_init(&sh.v_full[b], 1);
             mbar_init(&sh.v_ready[b], 1);
-            mbar_init(&sh.k_empty[b], 2);  // both tiles' issuers
             mbar_init(&sh.v_empty[b], 2);
         }
         mbar_init(&sh.fin, 2);
@@ -192,9 +205,9 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
     int qi = 0, head = 0, lo = 0, hi = 0;
     bool live = false;
     if (warp < MSK_SOFTMAX_WARPS) {
-        qi = q0 + t * a.tq + row / a.gp;
+        qi = q0 + (halves ? 0 : t) * a.tq + row / a.gp;
         head = h0 + row % a.gp;
-        live = t < ntiles && row < a.tq * a.gp && qi < a.Lq;
+        live = (halves || t < ntiles) && row < a.tq * a.gp && qi < a.Lq;
         if (live) {
             lo = a.kv_begin ? max(0, __ldg(a.kv_begin + qi)) : 0;
             hi = a.kv_end ? min(a.Lk, __ldg(a.kv_end + qi)) : a.Lk;
@@ -232,6 +245,13 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
     }
 #pragma unroll
     for (int x = 0; x < 2; x++) t0[x] = max(t0[x], B0), t1[x] = min(t1[x], B1);  // empty where t0 >= t1
+    const int N = max(0, B1 - B0), mid = B0 + (N + 1) / 2;
+    if (halves) t0[0] = B0, t1[0] = t0[1] = mid, t1[1] = B1;
+    // The n-th block that is loaded: in order, or from the halves in turn; and whether tile x
+    // works on it, as its block number i.
+    auto block = [&](int n) { return halves ? ((n & 1) ? mid : B0) + (n >> 1) : B0 + n; };
+    auto owns = [&](int x, int n) { return halves ? (n & 1) == x : B0 + n >= t0[x] && B0 + n < t1[x]; };
+    auto local = [&](int x, int n) { return halves ? n >> 1 : B0 + n - t0[x]; };
     // A block that every row of both tiles sees whole needs no gate.
     auto whole = [&](int kb) { return kb * MSK_BK >= b_full0 && (kb + 1) * MSK_BK <= b_full1; };
 
@@ -245,33 +265,28 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
                 __syncwarp();
                 if (lane < 2) tma_load_3d(dst + lane * (MSK_KV / 2), map, 64 * lane, hk, kb * MSK_BK, full);
             };
-            for (int n = 0; n < B1 - B0; n++) {
-                const int b = n % MSK_SLOTS;
-                const uint32_t before = (n / MSK_SLOTS - 1) & 1;  // the slot's last use
-                if (n >= MSK_SLOTS && !__all_sync(~0u, att_wait(&sh.k_empty[b], before))) break;
-                load(sK + b * MSK_KV, &tk, &sh.k_full[b], B0 + n);
+            for (int n = 0; n < N; n++) {
+                const int b = n % MSK_SLOTS, c = v_slot(n);
+                if (n >= MSK_SLOTS && !__all_sync(~0u, att_wait(&sh.k_empty[b], (n / MSK_SLOTS - 1) & 1))) break;
+                load(sK + b * MSK_KV, &tk, &sh.k_full[b], block(n));
                 nk = n + 1;
-                if (n >= MSK_SLOTS && !__all_sync(~0u, att_wait(&sh.v_empty[b], before))) break;
-                load(sV + b * MSK_KV, &tv, &sh.v_full[b], B0 + n);
+                if (n >= v_slots && !__all_sync(~0u, att_wait(&sh.v_empty[c], v_use(n - v_slots)))) break;
+                load(sV + c * MSK_KV, &tv, &sh.v_full[c], block(n));
                 nv = n + 1;
             }
             // No copy may still be landing when the CTA exits, also when a wait ran out.
             if (lane == 0) {
-                auto drain = [&](uint64_t* full, int issued) {
-                    for (int m = issued > MSK_SLOTS ? issued - MSK_SLOTS : 0; m < issued; m++)
-                        drain_wait(&full[m % MSK_SLOTS], (m / MSK_SLOTS) & 1);
-                };
-                drain(sh.k_full, nk);
-                drain(sh.v_full, nv);
+                for (int m = max(0, nk - MSK_SLOTS); m < nk; m++) drain_wait(&sh.k_full[m % MSK_SLOTS], (m / MSK_SLOTS) & 1);
+                for (int m = max(0, nv - v_slots); m < nv; m++) drain_wait(&sh.v_full[v_slot(m)], v_use(m));
                 for (int x = 0; x < ntiles; x++) drain_wait(&sh.q_full[x], 0);
             }
             __syncwarp();
         } else if (warp == MSK_GATE_WARP) {
             // ------------------------------------------------------------ V's gate
-            for (int n = 0; n < B1 - B0; n++) {
-                const int b = n % MSK_SLOTS;
-                if (!__all_sync(~0u, att_wait(&sh.v_full[b], (n / MSK_SLOTS) & 1))) break;
-                if (!whole(B0 + n)) {
+            for (int n = 0; n < N; n++) {
+                const int b = v_slot(n);
+                if (!__all_sync(~0u, att_wait(&sh.v_full[b], v_use(n)))) break;
+                if (!whole(block(n))) {
                     if (lane < 2) sh.flags[b][lane] = 0;
                     __syncwarp();
                     uint4* const v = reinterpret_cast<uint4*>(sV + b * MSK_KV);
@@ -310,20 +325,21 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
             const int x = __shfl_sync(~0u, warp - MSK_MMA_WARP, 0);
             const uint32_t el = elect_one();
             const uint32_t tO = tm + 256 * x, tS = tO + 128;
-            const uint64_t dq = att_qk_desc(sQ) + (uint64_t)(x * (ATT_TILE >> 4)), dk = att_qk_desc(sK);
+            const int xq = halves ? 0 : x;  // whose queries
+            const uint64_t dq = att_qk_desc(sQ) + (uint64_t)(xq * (ATT_TILE >> 4)), dk = att_qk_desc(sK);
             const uint64_t dv = sdesc_sw128(smem_u32(sV), MSK_KV / 2, 1024);
-            const int kb0 = x ? t0[1] : t0[0], kb1 = x ? t1[1] : t1[0];
             bool ok = true;
             auto wait = [&](uint64_t* bar, uint32_t parity) { ok = ok && __all_sync(~0u, att_wait(bar, parity)); };
-            // S(kb) of the n-th block.  A block outside the tile's range is waited for all the
-            // same before its slot is given back.
+            // S of the n-th block.  A block that is not the tile's is waited for all the same
+            // before its slot is given back.
             auto scores = [&](int n) {
-                const int kb = B0 + n, b = n % MSK_SLOTS, sl = (kb - kb0) & 1;
-                if (kb >= B1) return;
+                const int b = n % MSK_SLOTS;
+                if (n >= N) return;
                 wait(&sh.k_full[b], (n / MSK_SLOTS) & 1);
                 if (!ok) return;
-                if (kb >= kb0 && kb < kb1) {
+                if (owns(x, n)) {
                     tc_fence_after();
+                    const int sl = local(x, n) & 1;
                     const uint64_t d = dk + (uint64_t)(b * (MSK_KV >> 4));
                     const uint32_t ts = tS + 64 * sl;
                     mma_f16_ss_if(el, ts, dq, d, ID_S, 0);
@@ -334,27 +350,32 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
                 }
                 if (el) tc_commit(&sh.k_empty[b]);
             };
-            if (kb0 < kb1) wait(&sh.q_full[x], 0);
-            if (ok) scores(0);
-            if (ok) scores(1);
-            for (int n = 0; ok && n < B1 - B0; n++) {
-                const int kb = B0 + n, b = n % MSK_SLOTS, sl = (kb - kb0) & 1;
-                wait(&sh.v_ready[b], (n / MSK_SLOTS) & 1);
-                if (kb >= kb0 && kb < kb1) {
-                    wait(&sh.p_full[x][sl], ((kb - kb0) >> 1) & 1);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t d = dv + (uint64_t)(b * (MSK_KV >> 4));
-                    const uint32_t tp = tS + 64 * sl;
-                    mma_f16_ts_if(el, tO, tp, d, ID_O, kb > kb0);
+            if (t0[0] < t1[0] || t0[1] < t1[1]) {
+                if (xq < ntiles) wait(&sh.q_full[xq], 0);
+            }
+            const int ahead = halves ? 4 : 2;  // two of the tile's own blocks
+#pragma unroll 1
+            for (int n = -ahead; ok && n < N; n++) {
+                if (n >= 0) {
+                    const int b = v_slot(n);
+                    wait(&sh.v_ready[b], v_use(n));
+                    if (owns(x, n)) {
+                        const int i = local(x, n), sl = i & 1;
+                        wait(&sh.p_full[x][sl], (i >> 1) & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t d = dv + (uint64_t)(b * (MSK_KV >> 4));
+                        const uint32_t tp = tS + 64 * sl;
+                        mma_f16_ts_if(el, tO, tp, d, ID_O, i > 0);
 #pragma unroll
-                    for (int kk = 1; kk < MSK_BK / 16; kk++)
-                        mma_f16_ts_if(el, tO, tp + 8 * kk, d + att_v_step(kk), ID_O, 1);
-                    if (el) tc_commit(&sh.o_done[x][sl]);
+                        for (int kk = 1; kk < MSK_BK / 16; kk++)
+                            mma_f16_ts_if(el, tO, tp + 8 * kk, d + att_v_step(kk), ID_O, 1);
+                        if (el) tc_commit(&sh.o_done[x][sl]);
+                    }
+                    if (!ok) break;
+                    if (el) tc_commit(&sh.v_empty[b]);
                 }
-                if (!ok) break;
-                if (el) tc_commit(&sh.v_empty[b]);
-                scores(n + 2);
+                scores(n + ahead);
             }
             // Every MMA issued above completes before tensor memory is released.
             if (el) {
@@ -468,8 +489,8 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
             }
             if (!unseen && !whole(kb)) {  // V's gate: a marked key of the row's own?
                 // (before P is handed over: after that the slot may be refilled)
-                const int n = kb - B0, b = n % MSK_SLOTS;
-                if (!__all_sync(~0u, att_wait(&sh.v_ready[b], (n / MSK_SLOTS) & 1))) l = NAN;
+                const int n = halves ? 2 * (kb - kb0) + t : kb - B0, b = v_slot(n);
+                if (!__all_sync(~0u, att_wait(&sh.v_ready[b], v_use(n)))) l = NAN;
 #pragma unroll 1
                 for (int w = 0; w < 2; w++)
                     for (uint32_t f = sh.flags[b][w]; f; f &= f - 1)
@@ -480,36 +501,66 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.p_full[t][sl]);
         }
-        const bool ran = kb0 < kb1;
-        if (ran && ok) ok = __all_sync(~0u, att_wait(&sh.o_done[t][(kb1 - 1 - kb0) & 1], ((kb1 - 1 - kb0) >> 1) & 1));
-        // a tile without a block: its queries' copy must have landed before the space is used again
-        if (!ran && t < ntiles) ok = __all_sync(~0u, att_wait(&sh.q_full[t], 0));
+        // The last P V of a tile with blocks.
+        auto last = [&](int x) {
+            const int i = (x ? t1[1] - t0[1] : t1[0] - t0[0]) - 1;
+            return i < 0 || __all_sync(~0u, att_wait(&sh.o_done[x][i & 1], (i >> 1) & 1));
+        };
+        if (ok) ok = last(t);
+        // O = f O_t (+ fx O_other): halves join their results, in the scale of the larger maximum.
+        const bool ran = kb0 < kb1, ran_x = halves && t0[t ^ 1] < t1[t ^ 1];
+        float f = 1.0f, fx = 0.0f;
+        if (halves) {
+            if (ok) ok = last(t ^ 1);
+            sh.ml[t][row] = ran ? make_float2(m, l) : make_float2(-INFINITY, 0.0f);
+            ok = named_barrier_and(1 + quad, 64, ok);
+            const float2 o = sh.ml[t ^ 1][row];
+            if (!ran) m = -INFINITY, l = 0.0f;
+            const float top = fmaxf(m, o.x), zero = top == -INFINITY ? 0.0f : top;
+            f = att_ex2(m - zero);
+            fx = att_ex2(o.x - zero);
+            l = l * f + o.y * fx;
+            m = top;
+        }
+        const bool any = some && (ran || ran_x);
+        // Without a block: the queries' copy must have landed before their space is used again.
+        if (!ran && !ran_x && (halves || t < ntiles)) ok = ok && __all_sync(~0u, att_wait(&sh.q_full[halves ? 0 : t], 0));
         if (ok) {
             tc_fence_after();
             const int64_t at = (int64_t)qi * a.H + head;
             const bool split = a.splits > 1;
             const int64_t pat = (int64_t)blockIdx.y * a.Lq * a.H + at;
-            const float inv = some && ran ? (split ? 1.0f : 1.0f / l) : 0.0f;
-            if (split && live) a.part_ml[pat] = some && ran ? make_float2(m, l) : make_float2(-INFINITY, 0.0f);
-            // O through shared memory (this warp's 8 KB of its tile's queries, which no MMA
-            // reads any more), so that a store covers two whole rows of 256 bytes: 32 rows of
-            // 16 bytes keep the store unit busy for 32 cycles (4000 in all for a CTA).  Rows
-            // of 16 chunks, chunk c of row i at c ^ (i & 15).
+            const float inv = split ? 1.0f : 1.0f / l;
+            f *= inv;
+            fx *= inv;
+            if (split && live && !(halves && t)) a.part_ml[pat] = any ? make_float2(m, l) : make_float2(-INFINITY, 0.0f);
+            // 64 columns at a time (halves: one each) through shared memory (8 KB a warp of the
+            // queries' and, with one tile, the keys' space, which nothing reads any more), so that a store covers whole
+            // lines: 32 rows of 16 bytes keep the store unit busy for 32 cycles.  Rows of 256
+            // bytes, 16-byte chunk c of row i at c ^ (i & 15).  Small loops: this code runs once.
             const bool f32 = split || !a.o_f16;
             uint8_t* const buf = sQ + t * ATT_TILE + quad * 8192;
-            const int64_t mine = live && !(split && !ran) ? (split ? pat : at) : -1;
+            uint8_t* const out = static_cast<uint8_t*>(split ? static_cast<void*>(a.part) : a.o);
+            const int64_t mine = live && !(split && !ran && !ran_x) ? (split ? pat : at) : -1;
+            const uint32_t tX = tm + ((uint32_t)(32 * quad) << 16) + 256 * (t ^ 1);
 #pragma unroll 1
-            for (int c = 0; c < (f32 ? 2 : 1); c++) {  // f32: 64 columns at a time
-// (small loops: this code runs once per CTA, so its time is that of fetching it)
+            for (int g = halves ? t : 0; g < (halves ? t + 1 : 2); g++) {
 #pragma unroll 1
-                for (int d = 0; d < (f32 ? 4 : 8); d++) {
+                for (int d = 0; d < 4; d++) {
                     float r[16];
                     if (ran) {
-                        tmem_ld16(tO + 64 * c + 16 * d, reinterpret_cast<uint32_t*>(r));
+                        tmem_ld16(tO + 64 * g + 16 * d, reinterpret_cast<uint32_t*>(r));
                         tmem_wait_ld();
                     }
 #pragma unroll
-                    for (int e = 0; e < 16; e++) r[e] = some && ran ? r[e] * inv : 0.0f;
+                    for (int e = 0; e < 16; e++) r[e] = any && ran ? r[e] * f : 0.0f;
+                    if (ran_x) {
+                        float y[16];
+                        tmem_ld16(tX + 64 * g + 16 * d, reinterpret_cast<uint32_t*>(y));
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; e++) r[e] = any ? fmaf(y[e], fx, r[e]) : 0.0f;
+                    }
                     auto put = [&](int chunk, uint4 x) {
                         *reinterpret_cast<uint4*>(buf + lane * 256 + ((chunk ^ (lane & 15)) * 16)) = x;
                     };
@@ -526,14 +577,13 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
                     }
                 }
                 __syncwarp();
-                uint8_t* const out = static_cast<uint8_t*>(split ? static_cast<void*>(a.part) : a.o);
-                const int row_bytes = f32 ? 512 : 256;
+                const int per = f32 ? 16 : 8;  // chunks of a row
 #pragma unroll 2
-                for (int i = 0; i < 16; i++) {
-                    const int rw = 2 * i + (lane >> 4), chunk = lane & 15;
+                for (int i = 0; i < per; i++) {
+                    const int c = i * 32 + lane, rw = c / per, chunk = c % per;
                     const int64_t to = __shfl_sync(~0u, mine, rw);
                     if (to < 0) continue;
-                    *reinterpret_cast<uint4*>(out + to * row_bytes + 256 * c + chunk * 16) =
+                    *reinterpret_cast<uint4*>(out + (to * 2 + g) * (16 * per) + chunk * 16) =
                         *reinterpret_cast<const uint4*>(buf + rw * 256 + ((chunk ^ (rw & 15)) * 16));
                 }
                 __syncwarp();

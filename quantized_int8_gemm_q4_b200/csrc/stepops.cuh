@@ -50,7 +50,7 @@ struct MaskPlan {
 
 // Tiles, CTAs and key parts of a masked attention call.  Two query tiles per CTA once one
 // each would need more than one wave; with at most half a wave of CTAs the keys are cut
-// into parts of at least four blocks, up to one wave in all.
+// into parts of at least eight blocks, up to one wave in all.
 MaskPlan mask_plan(int64_t Lq, int64_t Lk, int64_t H, int64_t Hkv, int sms) {
     MaskPlan p;
     const int group = (int)(H / Hkv);
@@ -61,9 +61,9 @@ MaskPlan mask_plan(int64_t Lq, int64_t Lk, int64_t H, int64_t Hkv, int sms) {
     p.tiles = n_tiles * n_heads > sms ? 2 : 1;
     p.grid = (n_tiles + p.tiles - 1) / p.tiles * n_heads;
     p.splits = 1;
-    if (2 * p.grid <= sms && blocks >= 8) {
+    if (2 * p.grid <= sms && blocks >= 16) {
         const int64_t most = sms / p.grid;
-        p.splits = (int)(most < blocks / 4 ? most : blocks / 4);
+        p.splits = (int)(most < blocks / 8 ? most : blocks / 8);
     }
     p.ml_off = p.bytes = 0;
     if (p.splits > 1) {
@@ -75,18 +75,21 @@ MaskPlan mask_plan(int64_t Lq, int64_t Lk, int64_t H, int64_t Hkv, int sms) {
 
 bool g_mask_attr_done[MAX_DEV];
 
+typedef void (*MaskKernel)(CUtensorMap, CUtensorMap, CUtensorMap, MaskArgs);
+
 template <int MODE>
 bool mask_attribute() {
     cudaFuncAttributes fa;
     return cudaFuncSetAttribute(attention_masked_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)MSK_SMEM) == cudaSuccess &&
+                                (int)msk_smem(MODE & 4)) == cudaSuccess &&
            cudaFuncGetAttributes(&fa, attention_masked_kernel<MODE>) == cudaSuccess &&
            fa.numRegs >= MSK_REG_LAUNCH;  // the warpgroups' setmaxnreg split must fit in the launch's registers
 }
 
 bool mask_attributes(int dev) {
     if (!g_mask_attr_done[dev])
-        g_mask_attr_done[dev] = mask_attribute<0>() && mask_attribute<1>() && mask_attribute<2>() && mask_attribute<3>();
+        g_mask_attr_done[dev] = mask_attribute<0>() && mask_attribute<1>() && mask_attribute<2>() && mask_attribute<3>() &&
+                                mask_attribute<4>() && mask_attribute<5>() && mask_attribute<6>() && mask_attribute<7>();
     return g_mask_attr_done[dev];
 }
 
@@ -223,7 +226,7 @@ int dllm_attention_masked(const void* q, int64_t ldq, const void* k, int64_t ldk
     MaskArgs a;
     memset(&a, 0, sizeof(a));
     a.Lq = (int32_t)Lq, a.Lk = (int32_t)Lk, a.H = (int32_t)H, a.group = (int32_t)(H / Hkv);
-    a.gp = p.gp, a.tq = p.tq, a.tiles = p.tiles, a.splits = p.splits;
+    a.gp = p.gp, a.tq = p.tq, a.splits = p.splits;
     a.kv_begin = kv_begin, a.kv_end = kv_end, a.q_pos = q_pos;
     const double scale = 0.08838834764831844, log2e = 1.4426950408889634;  // 1 / sqrt(128)
     a.cap_in = softcap > 0.0f ? (float)(scale / softcap) : 0.0f;
@@ -234,12 +237,11 @@ int dllm_attention_masked(const void* q, int64_t ldq, const void* k, int64_t ldk
     a.part = static_cast<float*>(workspace);
     a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + p.ml_off);
     const dim3 grid((unsigned)p.grid, (unsigned)p.splits);
-    const int mode = (softcap > 0.0f ? 1 : 0) + (slopes ? 2 : 0);
-    const auto kernel = mode == 0   ? attention_masked_kernel<0>
-                        : mode == 1 ? attention_masked_kernel<1>
-                        : mode == 2 ? attention_masked_kernel<2>
-                                    : attention_masked_kernel<3>;
-    rc = status_of(launch_pdl(kernel, grid, dim3(MSK_THREADS), MSK_SMEM, s, tq, tk, tv, a));
+    static const MaskKernel kernels[8] = {attention_masked_kernel<0>, attention_masked_kernel<1>, attention_masked_kernel<2>,
+                                          attention_masked_kernel<3>, attention_masked_kernel<4>, attention_masked_kernel<5>,
+                                          attention_masked_kernel<6>, attention_masked_kernel<7>};
+    const MaskKernel kernel = kernels[(softcap > 0.0f ? 1 : 0) + (slopes ? 2 : 0) + (p.tiles == 1 ? 4 : 0)];
+    rc = status_of(launch_pdl(kernel, grid, dim3(MSK_THREADS), msk_smem(p.tiles == 1), s, tq, tk, tv, a));
     if (rc || p.splits == 1) return rc;
     return status_of(launch_pdl(attention_masked_join_kernel, dim3((unsigned)((Lq * H + 3) / 4)), dim3(128), 0, s, a.part,
                                 a.part_ml, Lq * H, p.splits, o, a.o_f16));
