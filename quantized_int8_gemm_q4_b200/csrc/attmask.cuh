@@ -614,17 +614,32 @@ __global__ void __launch_bounds__(128) attention_masked_join_kernel(const float*
     for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, d));
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     float l = 0.0f;
-    for (int z = 0; z < splits; z++) {
-        const float2 x = ml[z * rows + at];
-        if (x.x == -INFINITY) continue;
-        const float w = att_ex2(x.x - M);
-        const float4 p = reinterpret_cast<const float4*>(part + (z * rows + at) * ATT_DH)[lane];
+    for (int z0 = 0; z0 < splits; z0 += 32) {
+        // lane z: the part's weight (0 where it has no key of the row: its O is not written)
+        const int z = z0 + lane;
+        const float2 x = z < splits ? ml[z * rows + at] : make_float2(-INFINITY, 0.0f);
+        const float w = x.x == -INFINITY ? 0.0f : att_ex2(x.x - M);
         l = fmaf(w, x.y, l);
-        acc.x = fmaf(w, p.x, acc.x);
-        acc.y = fmaf(w, p.y, acc.y);
-        acc.z = fmaf(w, p.z, acc.z);
-        acc.w = fmaf(w, p.w, acc.w);
+        for (int j = 0; j < min(32, splits - z0); j += 8) {  // eight loads in flight
+            float4 p[8];
+            float wj[8];
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                wj[e] = __shfl_sync(~0u, w, j + e);
+                p[e] = wj[e] > 0.0f ? reinterpret_cast<const float4*>(part + ((z0 + j + e) * rows + at) * ATT_DH)[lane]
+                                    : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                acc.x = fmaf(wj[e], p[e].x, acc.x);
+                acc.y = fmaf(wj[e], p[e].y, acc.y);
+                acc.z = fmaf(wj[e], p[e].z, acc.z);
+                acc.w = fmaf(wj[e], p[e].w, acc.w);
+            }
+        }
     }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
     const float inv = M == -INFINITY ? 0.0f : 1.0f / l;
     if (o_f16)
         reinterpret_cast<uint2*>(static_cast<__half*>(o) + at * ATT_DH)[lane] =
