@@ -73,7 +73,7 @@ struct MaskArgs {
     int32_t gp, tq;   // heads and queries per tile
     int32_t splits;   // parts of the key range (grid y)
     const int32_t *kv_begin, *kv_end, *q_pos;
-    float cap_in, cap_out;  // s' = cap_out tanh(cap_in qk), in base-2 exponents
+    float cap_in, cap_out;  // base-2 exponents: cap_out tanh(cap_in q.k)
     const float* slopes;
     void* o;
     int32_t o_f16;
@@ -87,6 +87,13 @@ __device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
         : "=l"(d)
         : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)),
           "l"(*reinterpret_cast<uint64_t*>(&c)));
+    return *reinterpret_cast<float2*>(&d);
+}
+__device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(d)
+        : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
     return *reinterpret_cast<float2*>(&d);
 }
 __device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
@@ -136,6 +143,20 @@ __device__ __forceinline__ void mma_f16_ts_if(uint32_t issue, uint32_t d_tmem, u
 __device__ __forceinline__ float att_tanh(float y) {
     const float e = att_ex2(y * 2.885390081777927f);
     return 1.0f - __fdividef(2.0f, 1.0f + e);
+}
+
+// tanh of two values of at most 1 on the multiply-add pipe: an odd polynomial of degree 13
+// fitted to it, off by less than 2^-23.
+__device__ __forceinline__ float2 att_tanh_poly(float2 y) {
+    auto k = [](float c) { return make_float2(c, c); };
+    const float2 q = fmul2(y, y);
+    float2 p = ffma2(q, k(0.0009637725888751447f), k(-0.005951281636953354f));
+    p = ffma2(p, q, k(0.019973283633589745f));
+    p = ffma2(p, q, k(-0.05326583608984947f));
+    p = ffma2(p, q, k(0.13319583237171173f));
+    p = ffma2(p, q, k(-0.33332130312919617f));
+    p = ffma2(p, q, k(0.9999997019767761f));
+    return fmul2(p, y);
 }
 
 // MODE bit 0: cap, bit 1: distance bias, bit 2: halves.
@@ -419,16 +440,30 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
                 for (int c = 0; c < 4; c++) tmem_ld16(tS + 16 * c, reinterpret_cast<uint32_t*>(s) + 16 * c);
                 tmem_wait_ld();
                 if constexpr (CAP) {
+                    // s = tanh(cap_in s); where every score of the warp is below the cap, as
+                    // scores mostly are, without the special-function unit, which the
+                    // exponentials need (three of its operations per score otherwise)
+                    float big[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                    for (int j = 0; j < MSK_BK; j++) s[j] = a.cap_out * att_tanh(s[j] * a.cap_in);
-                } else if constexpr (BIAS) {
+                    for (int j = 0; j < MSK_BK; j++) big[j & 3] = fmaxf(big[j & 3], fabsf(s[j]));
+                    const float most = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3])) * a.cap_in;
+                    if (__all_sync(~0u, most <= 1.0f)) {
+                        const float2 c2 = make_float2(a.cap_in, a.cap_in);
 #pragma unroll
-                    for (int j = 0; j < MSK_BK; j++) s[j] *= ATT_C;
+                        for (int j = 0; j < MSK_BK; j += 2) {
+                            const float2 y = att_tanh_poly(fmul2(make_float2(s[j], s[j + 1]), c2));
+                            s[j] = y.x;
+                            s[j + 1] = y.y;
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < MSK_BK; j++) s[j] = att_tanh(s[j] * a.cap_in);
+                    }
                 }
                 if constexpr (BIAS) {
-                    const float d = (float)((int64_t)qp - k0);
+                    const float d = (float)((int64_t)qp - k0), c = CAP ? a.cap_out : ATT_C;
 #pragma unroll
-                    for (int j = 0; j < MSK_BK; j++) s[j] = fmaf(-slope, fabsf(d - (float)j), s[j]);
+                    for (int j = 0; j < MSK_BK; j++) s[j] = fmaf(-slope, fabsf(d - (float)j), s[j] * c);
                 }
                 if (k0 < w_lo1 || k0 + MSK_BK > w_hi0) {  // warp-uniform: some row hides some key
                     const int from = lo - k0, n = hi - lo;
@@ -443,14 +478,15 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
                 for (int j = 8; j < MSK_BK; j += 8)
 #pragma unroll
                     for (int e = 0; e < 4; e++) mx[e] = max3f(mx[e], s[j + e], s[j + 4 + e]);
-                constexpr float C = CAP || BIAS ? 1.0f : ATT_C;
+                const float C = BIAS ? 1.0f : CAP ? a.cap_out : ATT_C;
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * C;
                 const bool raise = top > m + ATT_RESCALE_LOG2;  // also from -inf; not where all is hidden
                 if (__any_sync(~0u, raise)) {
                     const float alpha = raise ? att_ex2(m - top) : 1.0f;  // 0 from -inf
+                    const bool had = __any_sync(~0u, raise && m != -INFINITY);  // else those rows of O are zeros
                     if (raise) m = top;
                     l *= alpha;
-                    if (kb > kb0) {
+                    if (had) {
                         // O must hold the blocks before this one
                         ok = __all_sync(~0u, att_wait(&sh.o_done[t][sl ^ 1], ((kb - 1 - kb0) >> 1) & 1));
                         if (!ok) break;
@@ -476,7 +512,7 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
 #pragma unroll
                     for (int e = 0; e < 16; e++) {
                         float2 x = make_float2(s[32 * c + 2 * e], s[32 * c + 2 * e + 1]);
-                        x = CAP || BIAS ? fadd2(x, n2) : ffma2(x, c2, n2);
+                        x = BIAS ? fadd2(x, n2) : ffma2(x, c2, n2);
                         x.x = att_ex2(x.x);
                         x.y = att_ex2(x.y);
                         sum[e & 1] = fadd2(sum[e & 1], x);
