@@ -336,7 +336,7 @@ int dllm_attention(const void* q, const void* k, const void* v, int64_t Lq, int6
  *   n_rot <= dh (0: no rotation).  pos: device int32 [L], any value; NULL means 0 .. L - 1.
  *   turns: device.  gamma_q, gamma_k: device f32 [dh], each may be NULL; with one given,
  *   eps > 0.  oq f16 [L][H][dh], ok and ov f16 [L][Hkv][dh], contiguous, may not overlap
- *   the inputs.  L == 0 is a no-op.
+ *   the inputs.  H, Hkv <= 65535.  L == 0 is a no-op.
  *   Arithmetic: the angle's turns in f64, reduced by the nearest whole number (every int32
  *   position keeps an angle good to 2^-24 of a turn); norm sum and rotation in f32; one
  *   rounding to f16 (|x| above 65504 becomes an infinity).
@@ -369,7 +369,7 @@ int dllm_qk_rope(const float* q, int64_t ldq, const float* k, int64_t ldk, const
  * reads key head h / (H / Hkv); ld >= heads * dh, ld % 8 == 0, so k and v may lie in a
  * longer cache or in one fused buffer.  kv_begin, kv_end: device int32 [Lq]; NULL means 0,
  * Lk; values are clamped to [0, Lk].  q_pos: device int32 [Lq], the queries' key positions
- * (read with slopes only); NULL means i + Lk - Lq.  softcap >= 0, finite; slopes: device f32 [H] or
+ * (read with slopes only); NULL means i + Lk - Lq.  softcap: 0 or 2^-100 .. 2^100; slopes: device f32 [H] or
  * NULL.  o: [Lq][H][dh] contiguous, f32 (what dllm_quantize_act reads) or f16 by o_type, may not
  * overlap the inputs.  dh must be 128.  Lq == 0 is a no-op; Lk == 0 writes zeros.
  * What keys hold outside a query's interval (NaN, infinities, memory never written) does

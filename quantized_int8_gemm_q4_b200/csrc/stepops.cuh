@@ -16,7 +16,7 @@ cudaError_t launch_rope(const RopeArgs& a, dim3 grid, bool neox, cudaStream_t s)
                 : launch_pdl(qk_rope_kernel<G, false>, grid, dim3(ROPE_THREADS), 0, s, a);
 }
 
-bool g_sample_attr_done[MAX_DEV];
+bool g_sample_attr_done[MAX_DEV], g_sample_cluster16[MAX_DEV];
 
 int status_of(cudaError_t e) {
     if (e != cudaSuccess) {
@@ -145,7 +145,7 @@ int dllm_qk_rope(const float* q, int64_t ldq, const float* k, int64_t ldk, const
     if (L < 0 || H <= 0 || Hkv <= 0 || dh <= 0 || dh > 256 || dh % 8 || n_rot < 0 || n_rot > dh || n_rot % 8)
         return DLLM_ERR_ARG;
     if (layout != DLLM_ROPE_NORM && layout != DLLM_ROPE_NEOX) return DLLM_ERR_ARG;
-    if (H > (1 << 20) || Hkv > (1 << 20) || L > (1LL << 31) - 1) return DLLM_ERR_ARG;
+    if (H > 65535 || Hkv > 65535 || L > (1LL << 31) - 1) return DLLM_ERR_ARG;
     if (ldq < H * dh || ldk < Hkv * dh || (v && ldv < Hkv * dh)) return DLLM_ERR_ARG;
     if (!(std::fabs(mscale) < INFINITY)) return DLLM_ERR_ARG;
     if ((gamma_q || gamma_k) && (!(eps > 0.0f) || !(eps < INFINITY))) return DLLM_ERR_ARG;
@@ -176,7 +176,6 @@ int dllm_qk_rope(const float* q, int64_t ldq, const float* k, int64_t ldk, const
     const int64_t parts = (a.T + slots - 1) / slots;
     a.chunk = L * parts <= 8LL * g_num_sms[dev] ? slots : a.T;
     const dim3 grid((unsigned)L, (unsigned)((a.T + a.chunk - 1) / a.chunk));
-    if (grid.y > 65535) return DLLM_ERR_ARG;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const bool neox = layout == DLLM_ROPE_NEOX;
     return status_of(G == 8 ? launch_rope<8>(a, grid, neox, s) : G == 16 ? launch_rope<16>(a, grid, neox, s)
@@ -199,7 +198,8 @@ int dllm_attention_masked(const void* q, int64_t ldq, const void* k, int64_t ldk
                           dllm_ftype o_type, void* workspace, size_t workspace_bytes, dllm_stream_t stream) {
     if (Lq < 0 || Lk < 0 || H <= 0 || Hkv <= 0 || H % Hkv || dh != ATT_DH) return DLLM_ERR_ARG;
     if (o_type != DLLM_F32 && o_type != DLLM_F16) return DLLM_ERR_ARG;
-    if (!(softcap >= 0.0f) || !(softcap < INFINITY)) return DLLM_ERR_ARG;
+    // a cap whose reciprocal or base-2 form leaves f32 is refused
+    if (softcap != 0.0f && !(softcap >= 0x1p-100f && softcap <= 0x1p100f)) return DLLM_ERR_ARG;
     if (Lq > (1LL << 30) || Lk > (1LL << 30) || H > 65535) return DLLM_ERR_ARG;
     if (ldq < H * dh || ldk < Hkv * dh || ldv < Hkv * dh) return DLLM_ERR_ARG;
     if (ldq >= (1LL << 39) || ldk >= (1LL << 39) || ldv >= (1LL << 39)) return DLLM_ERR_ARG;  // tensor-map strides
@@ -260,10 +260,26 @@ int dllm_sample(const float* logits, int64_t R, int64_t V, int64_t ldl, const fl
     int rc = current_device(&dev);
     if (rc) return rc;
     const size_t most = 227 * 1024;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.blockDim = dim3(SMP_THREADS);
     if (!g_sample_attr_done[dev]) {
         if (cudaFuncSetAttribute(sample_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) != cudaSuccess ||
             cudaFuncSetAttribute(sample_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
             return DLLM_ERR_CUDA;
+        // clusters of 16 are not portable: asked for only where the device can hold one
+        cfg.gridDim = dim3(SMP_MAX_CLUSTER);
+        cfg.dynamicSmemBytes = most;
+        cfg.numAttrs = 1;
+        attr[0].val.clusterDim.x = SMP_MAX_CLUSTER;
+        int n = 0;
+        g_sample_cluster16[dev] = cudaOccupancyMaxActiveClusters(&n, sample_kernel, &cfg) == cudaSuccess && n > 0;
+        (void)cudaGetLastError();
         g_sample_attr_done[dev] = true;
     }
     SampleArgs a;
@@ -272,9 +288,11 @@ int dllm_sample(const float* logits, int64_t R, int64_t V, int64_t ldl, const fl
     a.V = V, a.ldl = ldl;
     a.temperature = temperature, a.top_k = top_k, a.top_p = top_p, a.min_p = min_p, a.u = u;
     a.token = token, a.conf = conf, a.entropy = entropy;
+    // CTAs per row: about 8192 elements each, up to 8 (up to 16 for a few rows of a large
+    // vocabulary, 22 -> 15 us for one of 152064 words).
     int C = 1;
     while (C < 8 && (int64_t)C * 8192 < V) C *= 2;
-    if (C == 8 && 16 * R <= g_num_sms[dev]) C = 16;
+    if (C == 8 && 16 * R <= g_num_sms[dev] && g_sample_cluster16[dev]) C = 16;
     a.slice = (int32_t)round_up((V + 3 + C - 1) / C, 128);
     // Two CTAs per SM where at least 3/4 of a slice then fits in shared memory (the rest is
     // read again from L2), else one.
@@ -284,19 +302,11 @@ int dllm_sample(const float* logits, int64_t R, int64_t V, int64_t ldl, const fl
     int bits = 0;
     while ((1LL << bits) < V) bits++;
     a.fix = 62 - bits < 51 ? 62 - bits : 51;
-    cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(C * R));
-    cfg.blockDim = dim3(SMP_THREADS);
     cfg.dynamicSmemBytes = sizeof(SampleShared) + (size_t)a.cached * 4;
     cfg.stream = reinterpret_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)C;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
     cfg.numAttrs = 2;
+    attr[0].val.clusterDim.x = (unsigned)C;
     return status_of(cudaLaunchKernelEx(&cfg, sample_kernel, a));
 }
 

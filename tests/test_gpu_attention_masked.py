@@ -176,7 +176,7 @@ def test_all_empty_and_no_keys():
         assert bool((o[:200] == 0).all()) and bool((o[200:] == 7).all())
 
 
-@pytest.mark.parametrize("cap", [0.5, 5.0, 30.0, 1000.0])
+@pytest.mark.parametrize("cap", [2.0 ** -100, 0.5, 5.0, 30.0, 1000.0, 1e9])
 @pytest.mark.parametrize("spread", [1.0, 3.0])
 def test_capped_scores(cap, spread):
     q, k, v = inputs(150, 400, 6, 3, 10, spread=spread)
@@ -209,7 +209,7 @@ def test_what_hidden_keys_hold_does_not_matter():
     """NaN, infinities and the type's lowest value in keys outside the intervals: between two
     documents of one tile, behind the last key, and everywhere for a padded query."""
     bad = [float("nan"), INF, -INF, -65504.0]
-    for H, Hkv in ((4, 4), (14, 2)):
+    for H, Hkv in ((4, 4), (14, 2), (64, 64)):  # the last: two query tiles per CTA
         L = 400
         q, k, v = inputs(L, L, H, Hkv, 15)
         b, e = documents([30, 0, 50], L)
@@ -227,6 +227,19 @@ def test_what_hidden_keys_hold_does_not_matter():
         lost[30:80] = True
         assert bool(torch.isfinite(o[~lost]).all())
         assert bool((~torch.isfinite(o[lost])).any(-1).all())
+
+
+def test_holes_in_a_long_prefix():
+    """Few queries, keys split over CTAs: each query sees one stretch of sound keys between bad ones."""
+    Lq, Lk = 8, 4000
+    for H, Hkv in ((4, 4), (28, 4)):
+        q, k, v = inputs(Lq, Lk, H, Hkv, 18)
+        b, e = t(np.arange(Lq) * 480 + 30), t(np.arange(Lq) * 480 + 30 + np.arange(Lq) * 60)
+        seen = torch.zeros(Lk, dtype=torch.bool, device="cuda")
+        for i in range(Lq):
+            seen[int(b[i]):int(e[i])] = True
+        k[~seen], v[~seen] = float("nan"), INF
+        check(q, k, v, b, e)
 
 
 def test_rows_in_a_fused_buffer_and_a_longer_cache():

@@ -98,6 +98,20 @@ def test_all_limits(V):
           mp=g.choice([0.0, 0.001, 0.05], R), u=g.uniform(0, 1, R))
 
 
+@pytest.mark.parametrize("R,V", [(1, 152064), (3, 126465), (9, 65537), (10, 70000), (2, 800000)])
+@pytest.mark.parametrize("spread", [0.3, 3.0])
+def test_few_rows_of_large_vocabularies(R, V, spread):
+    """Clusters of 16 (up to 9 rows on 148 SMs) and of 8; flat rows, whose limits keep thousands of
+    words, and peaked ones, whose limits keep a few."""
+    x, g = logits_of(R, V, 9, spread)
+    u = g.uniform(0, 1, R)
+    check(x, u=u)
+    check(x, k=g.integers(1, V, R), p=g.uniform(0.2, 1.0, R), u=u)
+    check(x, T=np.full(R, 0.7), k=g.integers(1, 200, R), p=g.uniform(0.2, 1.0, R), u=u)
+    check(x, p=g.uniform(0.2, 1.0, R), mp=np.full(R, 1e-4), u=u)
+    check(x, T=np.zeros(R), u=u)
+
+
 @pytest.mark.parametrize("limit", ["none", "k", "p", "mp", "greedy"])
 @pytest.mark.parametrize("V", [700, 30001])
 def test_each_limit_alone(limit, V):

@@ -75,7 +75,7 @@ ROPE_OK = (P, 512, P, 256, P, 256, 4, 4, 2, 128, P, P, 128, 0, 1.0, P, P, 1e-6, 
     dict(L=-1), dict(H=0), dict(Hkv=0), dict(dh=0), dict(dh=100), dict(dh=264), dict(n_rot=-8), dict(n_rot=12),
     dict(n_rot=136), dict(layout=1), dict(ldq=508), dict(ldk=252), dict(ldv=252), dict(mscale=math.inf),
     dict(mscale=math.nan), dict(eps=0.0), dict(eps=math.nan), dict(q=None), dict(k=None), dict(oq=None), dict(ok=None),
-    dict(ov=None), dict(turns=None), dict(L=1 << 31), dict(H=1 << 21),
+    dict(ov=None), dict(turns=None), dict(L=1 << 31), dict(H=65536, ldq=65536 * 128),
 ])
 def test_rope_arguments_refused(change):
     refuse("dllm_qk_rope", ROPE_OK, ROPE, change, dllm.DLLM_ERR_ARG)
@@ -95,7 +95,7 @@ ATT_OK = (P, 512, P, 256, P, 256, 4, 9, 4, 2, 128, P, P, P, 0.0, P, P, 1, P, 1 <
 
 @pytest.mark.parametrize("change", [
     dict(Lq=-1), dict(Lk=-1), dict(H=0), dict(Hkv=0), dict(H=3), dict(dh=64), dict(o_type=2), dict(softcap=-1.0),
-    dict(softcap=math.nan), dict(softcap=math.inf), dict(ldq=504), dict(ldk=248), dict(ldv=248), dict(q=None),
+    dict(softcap=math.nan), dict(softcap=math.inf), dict(softcap=1e-31), dict(softcap=2e30), dict(ldq=504), dict(ldk=248), dict(ldv=248), dict(q=None),
     dict(k=None), dict(v=None), dict(o=None), dict(Lq=(1 << 30) + 1), dict(Lk=(1 << 30) + 1), dict(H=65536),
 ])
 def test_attention_arguments_refused(change):
