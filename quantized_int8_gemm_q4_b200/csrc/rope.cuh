@@ -17,6 +17,12 @@
 // times turns, minus the nearest whole number): exact to 2^-24 of a turn for every int32
 // position, where an f32 product is off by whole turns.  Norm sums, rotation: f32; one
 // rounding to f16.
+//
+// Measured (one B200, launches replayed from a graph): 4096 positions of 32 + 32 + 32 heads of 128
+// with both norms 52.5 us, 5.75 TB/s, 0.89 of the measured copy rate; 1021 positions of 28 + 4 + 4
+// 7.6 us (0.57; 36 heads leave the last of three per thread mostly idle, and a quarter of the
+// instructions are the angles); 128 positions 3.4 us, one position 1.7 us (a launch).  Three heads
+// in flight per thread at 64 registers beat two (1021 positions: 8.8 us) and one (9.4).
 #pragma once
 
 #include "layout.cuh"

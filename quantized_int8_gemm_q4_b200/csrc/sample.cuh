@@ -23,8 +23,18 @@
 // What a step exchanges is written into every CTA of the cluster and evaluated by all of them
 // alike, so that no step waits for an answer.  A histogram is exchanged as 64 coarse sums;
 // the 32 bins behind the crossing one are then read from the other CTAs.
-// Bound: the logits' bytes; in practice the passes' arithmetic (the f64 exponentials) and the
-// cluster barriers between them.
+// Few candidates (up to 256 up to the end of a limit's bin, as min_p, top_k and peaked rows leave)
+// are gathered in one CTA, which ranks them and takes the token from them.
+// Bound: the logits' bytes; in practice the chain of passes and barriers (~38,000 cycles per
+// CTA where few candidates are left, two CTAs per SM) and, for flat rows, the weights: ~40
+// instructions an element, a third of them f64, and two to three shared-memory atomics of 4-5
+// cycles each.
+//
+// Measured (one B200): 1 row of 152064 words with all limits 14.2 us; 32 rows of 126464 with top_p
+// 60 us; 256 rows with all limits 158 us (0.82 TB/s).  Steps on the way: f64 exponentials of the math
+// library, a histogram per limit, 1024 threads 60 / 139 / 934 us; one histogram for both limits,
+// two CTAs per SM 39 / 79 / 385; weights by table 22 / 52 / 221; bulk copies and the list of few
+// candidates 15.5 / 62 / 177; 256 threads at 128 registers 14.4 / 60 / 158.
 #pragma once
 #include <cooperative_groups.h>
 
