@@ -41,7 +41,8 @@
 // Measured (one B200): 4096 positions under a 1000-position prefix, 32 heads: 156 us at 1965 MHz, 182 us
 // once the power cap holds the clock at 1680 MHz (800 TFLOP/s of attended pairs); six packed
 // documents over 1024 positions 16.5 us; one query over 20011 keys of 32 heads 61 us (5.3 TB/s);
-// 32 queries over 8200 keys, 28 heads on 4, 19 us; capped and biased, 1531 positions, 41 us.
+// 32 queries over 8200 keys, 28 heads on 4, 20 us; capped and biased, 1531 positions, 43 us (41 with
+// one choice of tanh per warp, which let hidden keys and other rows change a row's last bits).
 // Measured and not kept: 128-key blocks with one score slot (prefix 182 us against 157: S waits for P);
 // two threads per row, or the two slots' softmax on two warpgroups that hand the maximum over
 // (both 3-10% slower: the special-function unit is shared, the chains are longer); one
@@ -451,15 +452,22 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
 #pragma unroll
                 for (int c = 0; c < 4; c++) tmem_ld16(tS + 16 * c, reinterpret_cast<uint32_t*>(s) + 16 * c);
                 tmem_wait_ld();
+                const bool partial = k0 < w_lo1 || k0 + MSK_BK > w_hi0;  // warp-uniform: some row hides some key
+                const int from = lo - k0, shown = hi - lo;
                 if constexpr (CAP) {
-                    // s = tanh(cap_in s); where every score of the warp is below the cap, as
-                    // scores mostly are, without the special-function unit, which the
-                    // exponentials need (three of its operations per score otherwise)
+                    // s = tanh(cap_in s); where every score that the row sees is below the cap,
+                    // as scores mostly are, without the special-function unit, which the
+                    // exponentials need (three of its operations per score otherwise).  The
+                    // two ways round differently, so each row chooses by its own keys alone.
+                    if (partial)
+#pragma unroll
+                        for (int j = 0; j < MSK_BK; j++)
+                            if ((uint32_t)(j - from) >= (uint32_t)shown) s[j] = 0.0f;
                     float big[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                     for (int j = 0; j < MSK_BK; j++) big[j & 3] = fmaxf(big[j & 3], fabsf(s[j]));
                     const float most = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3])) * a.cap_in;
-                    if (__all_sync(~0u, most <= 1.0f)) {
+                    if (most <= 1.0f || !live) {
                         const float2 c2 = make_float2(a.cap_in, a.cap_in);
 #pragma unroll
                         for (int j = 0; j < MSK_BK; j += 2) {
@@ -477,12 +485,10 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
 #pragma unroll
                     for (int j = 0; j < MSK_BK; j++) s[j] = fmaf(-slope, fabsf(d - (float)j), s[j] * c);
                 }
-                if (k0 < w_lo1 || k0 + MSK_BK > w_hi0) {  // warp-uniform: some row hides some key
-                    const int from = lo - k0, n = hi - lo;
+                if (partial)
 #pragma unroll
                     for (int j = 0; j < MSK_BK; j++)
-                        if ((uint32_t)(j - from) >= (uint32_t)n) s[j] = -INFINITY;
-                }
+                        if ((uint32_t)(j - from) >= (uint32_t)shown) s[j] = -INFINITY;
                 float mx[4];
 #pragma unroll
                 for (int e = 0; e < 4; e++) mx[e] = fmaxf(s[e], s[4 + e]);
@@ -663,18 +669,19 @@ __global__ void __launch_bounds__(128) attention_masked_join_kernel(const float*
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     float l = 0.0f;
     for (int z0 = 0; z0 < splits; z0 += 32) {
-        // lane z: the part's weight (0 where it has no key of the row: its O is not written)
+        // lane z: the part's weight, -1 where it has no key of the row (a weight that underflows
+        // still takes its O: a NaN or an infinity there makes the row one)
         const int z = z0 + lane;
         const float2 x = z < splits ? ml[z * rows + at] : make_float2(-INFINITY, 0.0f);
-        const float w = x.x == -INFINITY ? 0.0f : att_ex2(x.x - M);
-        l = fmaf(w, x.y, l);
+        const float w = x.x == -INFINITY ? -1.0f : att_ex2(x.x - M);
+        l = fmaf(fmaxf(w, 0.0f), x.y, l);
         for (int j = 0; j < min(32, splits - z0); j += 8) {  // eight loads in flight
             float4 p[8];
             float wj[8];
 #pragma unroll
             for (int e = 0; e < 8; e++) {
                 wj[e] = __shfl_sync(~0u, w, j + e);
-                p[e] = wj[e] > 0.0f ? reinterpret_cast<const float4*>(part + ((z0 + j + e) * rows + at) * ATT_DH)[lane]
+                p[e] = !(wj[e] < 0.0f) ? reinterpret_cast<const float4*>(part + ((z0 + j + e) * rows + at) * ATT_DH)[lane]
                                     : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             }
 #pragma unroll

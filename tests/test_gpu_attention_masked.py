@@ -229,6 +229,45 @@ def test_what_hidden_keys_hold_does_not_matter():
         assert bool((~torch.isfinite(o[lost])).any(-1).all())
 
 
+@pytest.mark.parametrize("cap", [0.0, 3.0, 50.0])
+def test_hidden_keys_do_not_change_a_bit(cap):
+    """Hidden keys with scores far above the cap, with scores of zero, and not finite."""
+    for L, H, Hkv in ((500, 4, 4), (300, 64, 64), (200, 14, 2)):
+        q, k, v = inputs(L, L, H, Hkv, 19)
+        b, e = documents([90, 0, 33, 200], L)
+        e = torch.maximum(b, e - 7)  # each document's last keys are padding
+        seen = torch.zeros(L, dtype=torch.bool, device="cuda")
+        for i in range(L):
+            seen[int(b[i]):int(e[i])] = True
+        sl = torch.rand(H, device="cuda") * 0.1
+        outs = []
+        for x in (0.0, 300.0, float("nan")):
+            k[~seen], v[~seen] = x, x
+            outs.append(call(q, k, v, L, b, e, cap=cap, slopes=sl if cap == 3.0 else None)[:L].clone())
+        assert bool(torch.isfinite(outs[0].float()).all())
+        assert all(torch.equal(o, outs[0]) for o in outs[1:])
+    # the document next door: another one's keys do not matter to its rows either
+    q, k, v = inputs(256, 256, 2, 2, 20)
+    b, e = documents([40, 216], 256)
+    want = call(q, k, v, 256, b, e, cap=cap)[:40].clone()
+    k[40:] *= 50.0
+    assert torch.equal(call(q, k, v, 256, b, e, cap=cap)[:40], want)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), INF])
+def test_attended_keys_of_no_weight_still_count(bad):
+    """Scores 360 apart: the far keys' weights underflow in f32, within a CTA and where the key
+    range is split over CTAs; a value there that is not finite is still attended."""
+    for Lq, Lk, H, Hkv in ((2, 8000, 4, 4), (2, 500, 4, 4), (300, 500, 64, 8)):
+        q, k, v = inputs(Lq, Lk, H, Hkv, 23)
+        q[:], k[:100], k[100:] = 4.0, 4.0, -4.0
+        v[Lk - 300, :, 3] = bad
+        o = call(q, k, v, Lk)[:Lq].float()
+        assert not bool(torch.isfinite(o[:, :, 3]).any())
+        o[:, :, 3] = 0.0
+        assert bool(torch.isfinite(o).all())
+
+
 def test_holes_in_a_long_prefix():
     """Few queries, keys split over CTAs: each query sees one stretch of sound keys between bad ones."""
     Lq, Lk = 8, 4000
