@@ -431,18 +431,19 @@ __global__ void __launch_bounds__(SMP_THREADS, 2) sample_kernel(const __grid_con
     sm.table[threadIdx.x] = exp2((double)threadIdx.x / SMP_TABLE + a.fix);
     for (int i = threadIdx.x; i < SMP_BINS; i += SMP_THREADS) sm.cnt[i] = sm.lo[i] = sm.hi[i] = 0;
     __syncthreads();  // the barrier and the edges are there
+    bool bad = false;
     {
         const uint64_t t0 = globaltimer_ns();
         while (!mbar_try_wait(&sm.landed, 0))
             if (globaltimer_ns() - t0 > 2000000000ull) {
                 set_err(ERR_TIMEOUT);
+                bad = true;  // the whole cluster leaves: nothing is sampled from a slice that may still change
                 break;
             }
     }
 
     // the row's largest and smallest finite logit
     float hi = -INFINITY, lo = INFINITY;
-    bool bad = false;
     row.each(0, n, threadIdx.x, SMP_THREADS, [&](const float4& x, int) {
         const float xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -473,6 +474,7 @@ __global__ void __launch_bounds__(SMP_THREADS, 2) sample_kernel(const __grid_con
             if (a.entropy) a.entropy[i_row] = 0.0f;
             set_err(ERR_LOGITS);
         }
+        if (threadIdx.x == 0) drain_wait(&sm.landed, 0);  // no copy may land after the CTA's exit
         return;
     }
     row.scale = sm.scale;
