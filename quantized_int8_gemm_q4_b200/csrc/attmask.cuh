@@ -41,8 +41,8 @@
 // Measured (one B200): 4096 positions under a 1000-position prefix, 32 heads: 156 us at 1965 MHz, 182 us
 // once the power cap holds the clock at 1680 MHz (800 TFLOP/s of attended pairs); six packed
 // documents over 1024 positions 16.5 us; one query over 20011 keys of 32 heads 61 us (5.3 TB/s);
-// 32 queries over 8200 keys, 28 heads on 4, 20 us; capped and biased, 1531 positions, 43 us (41 with
-// one choice of tanh per warp, which let hidden keys and other rows change a row's last bits).
+// 32 queries over 8200 keys, 28 heads on 4, 20 us; capped and biased, 1531 positions in three documents, 40 us (43
+// with tanh of degree 13 only).
 // Measured and not kept: 128-key blocks with one score slot (prefix 182 us against 157: S waits for P);
 // two threads per row, or the two slots' softmax on two warpgroups that hand the maximum over
 // (both 3-10% slower: the special-function unit is shared, the chains are longer); one
@@ -158,8 +158,16 @@ __device__ __forceinline__ float att_tanh(float y) {
     return 1.0f - __fdividef(2.0f, 1.0f + e);
 }
 
-// tanh of two values of at most 1 on the multiply-add pipe: an odd polynomial of degree 13
-// fitted to it, off by less than 2^-23.
+// tanh of two values on the multiply-add pipe: odd polynomials fitted to it, of degree 7 up to
+// 0.35 (off by less than 2^-24) and of degree 13 up to 1 (2^-23).
+__device__ __forceinline__ float2 att_tanh_small(float2 y) {
+    auto k = [](float c) { return make_float2(c, c); };
+    const float2 q = fmul2(y, y);
+    float2 p = ffma2(q, k(-0.04837692156434059f), k(0.13283324241638184f));
+    p = ffma2(p, q, k(-0.3333165645599365f));
+    p = ffma2(p, q, k(0.9999998211860657f));
+    return fmul2(p, y);
+}
 __device__ __forceinline__ float2 att_tanh_poly(float2 y) {
     auto k = [](float c) { return make_float2(c, c); };
     const float2 q = fmul2(y, y);
@@ -467,8 +475,15 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
 #pragma unroll
                     for (int j = 0; j < MSK_BK; j++) big[j & 3] = fmaxf(big[j & 3], fabsf(s[j]));
                     const float most = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3])) * a.cap_in;
-                    if (most <= 1.0f || !live) {
-                        const float2 c2 = make_float2(a.cap_in, a.cap_in);
+                    const float2 c2 = make_float2(a.cap_in, a.cap_in);
+                    if (most <= 0.35f || !live) {
+#pragma unroll
+                        for (int j = 0; j < MSK_BK; j += 2) {
+                            const float2 y = att_tanh_small(fmul2(make_float2(s[j], s[j + 1]), c2));
+                            s[j] = y.x;
+                            s[j + 1] = y.y;
+                        }
+                    } else if (most <= 1.0f) {
 #pragma unroll
                         for (int j = 0; j < MSK_BK; j += 2) {
                             const float2 y = att_tanh_poly(fmul2(make_float2(s[j], s[j + 1]), c2));

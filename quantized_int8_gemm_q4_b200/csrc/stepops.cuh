@@ -50,15 +50,20 @@ struct MaskPlan {
 
 // Tiles, CTAs and key parts of a masked attention call.  Two query tiles per CTA once one
 // each would need more than one wave; with at most half a wave of CTAs the keys are cut
-// into parts of at least eight blocks, up to one wave in all.
-MaskPlan mask_plan(int64_t Lq, int64_t Lk, int64_t H, int64_t Hkv, int sms) {
+// into parts of at least eight blocks, up to one wave in all.  Three waves of one tile take
+// ~1.7 times as long as one of two, and two waves of two tiles twice as long, as far as the
+// softmax's chain and not the loading of keys sets the pace: with a cap or a bias (long_chain;
+// 32 heads, 1200 positions, capped: all keys 70.7 -> 59.5 us, eight documents 31.7 -> 29.8;
+// without either 53.3 -> 51.3 and 24.5 -> 26.4).
+MaskPlan mask_plan(int64_t Lq, int64_t Lk, int64_t H, int64_t Hkv, bool long_chain, int sms) {
     MaskPlan p;
     const int group = (int)(H / Hkv);
     p.gp = group < 128 ? group : 128;
     while (group % p.gp) p.gp--;
     p.tq = 128 / p.gp;
     const int64_t n_heads = H / p.gp, n_tiles = (Lq + p.tq - 1) / p.tq, blocks = (Lk + MSK_BK - 1) / MSK_BK;
-    p.tiles = n_tiles * n_heads > sms ? 2 : 1;
+    const int64_t waves = (n_tiles * n_heads + sms - 1) / sms;
+    p.tiles = waves == 1 || (waves == 3 && long_chain) ? 1 : 2;
     p.grid = (n_tiles + p.tiles - 1) / p.tiles * n_heads;
     p.splits = 1;
     if (2 * p.grid <= sms && blocks >= 16) {
@@ -188,7 +193,7 @@ int dllm_attention_masked_workspace_bytes(int64_t Lq, int64_t Lk, int64_t H, int
     int dev;
     int rc = current_device(&dev);
     if (rc) return rc;
-    *bytes = mask_plan(Lq, Lk, H, Hkv, g_num_sms[dev]).bytes;
+    *bytes = mask_plan(Lq, Lk, H, Hkv, false, g_num_sms[dev]).bytes;
     return DLLM_OK;
 }
 
@@ -215,7 +220,7 @@ int dllm_attention_masked(const void* q, int64_t ldq, const void* k, int64_t ldk
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (Lk == 0)
         return status_of(cudaMemsetAsync(o, 0, (size_t)(Lq * H * dh) * (o_type == DLLM_F16 ? 2 : 4), s));
-    const MaskPlan p = mask_plan(Lq, Lk, H, Hkv, g_num_sms[dev]);
+    const MaskPlan p = mask_plan(Lq, Lk, H, Hkv, softcap > 0.0f || slopes, g_num_sms[dev]);
     if (p.grid > (1LL << 31) - 1) return DLLM_ERR_ARG;
     if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes)) return DLLM_ERR_WORKSPACE;
     if (!mask_attributes(dev)) return DLLM_ERR_CUDA;

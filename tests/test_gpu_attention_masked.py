@@ -197,6 +197,18 @@ def test_distance_bias():
     check(qq, kk, vv, qp=t(np.arange(20) * 140 - 50), slopes=slopes)
 
 
+@pytest.mark.parametrize("Lq", [250, 420, 700, 900])
+def test_cap_and_bias_in_one_to_four_waves(Lq):
+    """64 heads x 2, 4, 6 and 8 query tiles; caps that leave scores below and above a third of them."""
+    H = 64
+    q, k, v = inputs(Lq, Lq, H, H, 24)
+    slopes = torch.rand(H, device="cuda") * 0.2
+    b, e = documents([Lq // 3, 40, Lq // 2 - 9], Lq)
+    check(q, k, v, b, e, cap=5.0)
+    check(q, k, v, b, e, cap=30.0, slopes=slopes)
+    check(q, k, v, b, e, slopes=slopes)
+
+
 def test_peaked_rows_and_raised_maxima():
     for Lq, H, Hkv in ((130, 2, 2), (300, 64, 8), (5, 14, 2)):
         check(*inputs(Lq, 640, H, Hkv, 13, spread=4.0))
