@@ -9,41 +9,47 @@
 // A tile is 128 rows (tensor-memory lanes) of one key head: gp query heads of its group
 // (the largest divisor of the group up to 128) x 128 / gp queries, row = query * gp + head,
 // which is the order in which one TMA box of gp heads x 128 / gp rows lands in shared memory.  So
-// grouped heads read their keys once, and one query of 8 heads fills 8 rows.  A CTA has two
-// tiles and the key blocks of 64 that any of their rows sees, or one of `splits` equal parts
-// of them.  In grids of less than a wave its two tiles are the same queries ("halves"): the
-// first takes the first half of the blocks, the second the others, and their results are
-// joined from tensor memory at the end, so that two chains of blocks run on each SM.  12 warps:
-//   warps 0-3, 4-7  softmax of tile 0, tile 1; thread = row, all 64 scores of a block in
+// grouped heads read their keys once, and one query of 8 heads fills 8 rows.  A CTA has one tile
+// and the key blocks of 64 that any of its rows sees, or one of `splits` equal parts of them.
+// Two chains of blocks run on each SM, in one of two ways:
+//   two CTAs      of 8 warps each share the SM (more tiles than SMs): one's start, masks and
+//                 output run beside the other's blocks
+//   halves        a CTA of 12 warps with two chains: the first takes the first half of the
+//                 blocks, the second the others, and their results are joined from tensor
+//                 memory at the end
+// Warps (of halves; the others' in brackets):
+//   0-3, 4-7 [0-3]  softmax of chain 0, chain 1; thread = row, all 64 scores of a block in
 //                   registers; the running maximum is raised by more than 2^8 at a time
-//   warp 8, 9       issue the MMAs of tile 0, tile 1 (S = Q K^T, O += P V; kind::f16, f32 in
-//                   tensor memory); warp 8 owns tensor memory.  The whole warp runs the
+//   8, 9 [4]        issue the MMAs of a chain (S = Q K^T, O += P V; kind::f16, f32 in
+//                   tensor memory); the first owns tensor memory.  The whole warp runs the
 //                   issue loop and an elected lane's predicate guards each instruction, so
 //                   that its operands stay in uniform registers: 75-97 cycles per MMA from
 //                   one warp against 141 inside a one-lane branch; two warps together issue
-//                   one per 64, the tensor core's rate.
-//   warp 10         TMA producer of Q, K and V (four slots each of 64 keys x dh)
-//   warp 11         V's gate: in a block that some row does not see whole, it replaces what
+//                   one per 64, the tensor core's rate.  [5 has nothing to do]
+//   10 [6]          TMA producer of Q, K and V (4 and 8 [2 and 3] slots of 64 keys x dh)
+//   11 [7]          V's gate: in a block that some row does not see whole, it replaces what
 //                   is not finite by zeros and marks those keys (a weight of zero times NaN is
 //                   NaN, and the hidden key of one row is another's); a row that attends a
 //                   marked key becomes NaN
-// Tensor memory: O_t at columns 256 t, two S slots of 64 columns behind it, block kb in slot
-// kb & 1; P lies over the first half of its S (f16 pairs).  Issue order per tile: S(0), S(1), then
+// Tensor memory: O of chain t at columns 256 t, two S slots of 64 columns behind it, block kb in slot
+// kb & 1; P lies over the first half of its S (f16 pairs).  Issue order per chain: S(0), S(1), then
 // P V(kb), S(kb + 2): the scores of the next block are there when a softmax ends, and the
-// tensor core works while the softmax of either tile runs.
+// tensor core works while the softmax of either chain runs.
 //
-// Bounds per pair of tiles and 128 keys: 2048 cycles of MMA at 8192 operations per cycle (2600
+// Bounds per SM, for two tiles and 128 keys: 2048 cycles of MMA at 8192 operations per cycle (2600
 // as issued: a 128 x 64 x 16 MMA takes 49 cycles for its 6 KB of shared memory), and 2048 of the
 // special-function unit (32768 exponentials at 16 per cycle).  A softmax thread's own chain (wait,
 // load, maximum, exponentials, store, hand-over) takes ~1900 cycles per block, and the two chains of
-// a pair run side by side: ~2000 cycles per block of both tiles.
+// an SM run side by side: ~2000 cycles per block of both.
 //
 // Measured (one B200): 4096 positions under a 1000-position prefix, 32 heads: 156 us at 1965 MHz, 182 us
 // once the power cap holds the clock at 1680 MHz (800 TFLOP/s of attended pairs); six packed
 // documents over 1024 positions 16.5 us; one query over 20011 keys of 32 heads 61 us (5.3 TB/s);
-// 32 queries over 8200 keys, 28 heads on 4, 20 us; capped and biased, 1531 positions in three documents, 40 us (43
-// with tanh of degree 13 only).
-// Measured and not kept: 128-key blocks with one score slot (prefix 182 us against 157: S waits for P);
+// 32 queries over 8200 keys, 28 heads on 4, 20 us; capped and biased, 1531 positions in three
+// documents, 39 us.
+// Measured and not kept: two tiles per CTA that share their key blocks (1200 positions of 32 heads,
+// all keys, 53 us against 42 for two CTAs; in eight documents 24.5 against 19.3; with the long
+// prefix the same); 128-key blocks with one score slot (prefix 182 us against 157: S waits for P);
 // two threads per row, or the two slots' softmax on two warpgroups that hand the maximum over
 // (both 3-10% slower: the special-function unit is shared, the chains are longer); one
 // exponential in four by polynomial (no gain) or in two (10% slower); all commits after the MMAs
@@ -55,31 +61,37 @@
 
 namespace dllm {
 
-constexpr int MSK_SOFTMAX_WARPS = 8;
-constexpr int MSK_MMA_WARP = 8, MSK_TMA_WARP = 10, MSK_GATE_WARP = 11;  // 8, 9: one per tile
-constexpr int MSK_THREADS = 32 * 12;
+constexpr int msk_threads(bool halves) { return halves ? 384 : 256; }
 constexpr int MSK_BK = 64;    // keys per block
-constexpr int MSK_SLOTS = 4;    // K slots, and V slots of two query tiles
-// Halves have one query tile, whose pair's space goes to V: with the scores of four blocks
-// ahead four V blocks wait for their weights, and as many are on their way.
-constexpr int MSK_V_SLOTS = 8;
+// Slots: with halves, the scores of four blocks ahead leave four V blocks waiting for their
+// weights, and as many are on their way.  Two CTAs per SM have the space of five slots each: K is
+// read two blocks ahead of its V.
+constexpr int MSK_K_SLOTS = 4, MSK_V_SLOTS = 8;  // at most
+constexpr int msk_k_slots(bool halves) { return halves ? 4 : 2; }
+constexpr int msk_v_slots(bool halves) { return halves ? 8 : 3; }
 constexpr int MSK_KV = MSK_BK * ATT_DH * 2;
 // Registers per thread after setmaxnreg (softmax warpgroups; the others), out of the
 // launch's 384 x 168.
-constexpr int MSK_REG_SOFTMAX = 200, MSK_REG_OTHER = 96, MSK_REG_LAUNCH = 168;
-static_assert(256 * MSK_REG_SOFTMAX + 128 * MSK_REG_OTHER <= MSK_THREADS * MSK_REG_LAUNCH, "setmaxnreg split");
+constexpr int MSK_REG_SOFTMAX = 200;
+constexpr int msk_reg_other(bool halves) { return halves ? 96 : 56; }
+constexpr int msk_reg_launch(bool halves) { return halves ? 168 : 128; }
+static_assert(256 * MSK_REG_SOFTMAX + 128 * msk_reg_other(true) <= 384 * msk_reg_launch(true), "setmaxnreg split");
+static_assert(128 * MSK_REG_SOFTMAX + 128 * msk_reg_other(false) <= 256 * msk_reg_launch(false), "setmaxnreg split");
 
 struct MaskShared {
-    uint64_t q_full[2], k_full[MSK_SLOTS], k_empty[MSK_SLOTS];
+    uint64_t q_full, k_full[MSK_K_SLOTS], k_empty[MSK_K_SLOTS];
     uint64_t v_full[MSK_V_SLOTS], v_ready[MSK_V_SLOTS], v_empty[MSK_V_SLOTS];
-    uint64_t s_full[2][2], p_full[2][2], o_done[2][2], fin;  // [tile][S slot]
+    uint64_t s_full[2][2], p_full[2][2], o_done[2][2], fin;  // [chain][S slot]
     uint32_t tmem, flags[MSK_V_SLOTS][2];  // per V slot, bit j: key j's value is not finite
     int32_t lo_min[8], hi_max[8], lo_max[8], hi_min[8];  // per softmax warp, over rows with keys
-    float2 ml[2][128];  // halves: each row's maximum and sum
+    float2 ml[2][128];  // halves only (the last field: without them it is not there)
 };
-// Q x2, K x4, V x4 or Q, K x4, V x8; barriers
-constexpr size_t msk_smem(bool halves) { return (halves ? 7 : 6) * (size_t)ATT_TILE + sizeof(MaskShared); }
+constexpr size_t msk_smem(bool halves) {
+    return ATT_TILE + (size_t)(msk_k_slots(halves) + msk_v_slots(halves)) * MSK_KV +
+           (halves ? sizeof(MaskShared) : offsetof(MaskShared, ml));
+}
 static_assert(msk_smem(true) <= 227 * 1024, "shared memory of a CTA");
+static_assert(2 * (msk_smem(false) + 1024) <= 228 * 1024, "shared memory of two CTAs");
 
 struct MaskArgs {
     int32_t Lq, Lk, H, group;
@@ -182,74 +194,69 @@ __device__ __forceinline__ float2 att_tanh_poly(float2 y) {
 
 // MODE bit 0: cap, bit 1: distance bias, bit 2: halves.
 template <int MODE>
-__global__ void __launch_bounds__(MSK_THREADS, 1)
+__global__ void __launch_bounds__(msk_threads(MODE & 4), MODE & 4 ? 1 : 2)
     attention_masked_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                             const __grid_constant__ CUtensorMap tv, const __grid_constant__ MaskArgs a) {
     constexpr bool CAP = MODE & 1, BIAS = MODE & 2, halves = MODE & 4;
     extern __shared__ __align__(1024) uint8_t smem[];
-    uint8_t* const sQ = smem;                                   // one or two tiles
-    uint8_t* const sK = smem + (halves ? 1 : 2) * ATT_TILE;     // four slots
-    uint8_t* const sV = sK + MSK_SLOTS * MSK_KV;                // v_slots slots
-    constexpr int v_log = halves ? 3 : 2, v_slots = 1 << v_log;
+    constexpr int CHAINS = halves ? 2 : 1;
+    constexpr int MMA_WARP = 4 * CHAINS, TMA_WARP = MMA_WARP + 2, GATE_WARP = MMA_WARP + 3;
+    constexpr int k_slots = msk_k_slots(halves), v_slots = msk_v_slots(halves);
+    uint8_t* const sQ = smem;
+    uint8_t* const sK = smem + ATT_TILE;
+    uint8_t* const sV = sK + k_slots * MSK_KV;
     MaskShared& sh = *reinterpret_cast<MaskShared*>(sV + v_slots * MSK_KV);
-    // Slot and parity of V block n.
-    auto v_slot = [&](int n) { return n & (v_slots - 1); };
-    auto v_use = [&](int n) { return (uint32_t)(n >> v_log) & 1; };
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // The last queries first (under causal intervals theirs are the longest), all heads of them.
     const int n_heads = a.H / a.gp, h0 = (int)(blockIdx.x % n_heads) * a.gp, hk = h0 / a.group;
-    const int q0 = (int)((gridDim.x - 1 - blockIdx.x) / n_heads) * (halves ? 1 : 2) * a.tq;
-    const int ntiles = !halves && a.Lq - q0 > a.tq ? 2 : 1;  // with queries of their own
+    const int q0 = (int)((gridDim.x - 1 - blockIdx.x) / n_heads) * a.tq;
 
-    if (warp == MSK_MMA_WARP) {
-        tmem_alloc(&sh.tmem, ATT_TM_COLS);
+    if (warp == MMA_WARP) {
+        tmem_alloc(&sh.tmem, 256 * CHAINS);
         tmem_relinquish();
     }
-    if (threadIdx.x == 32 * MSK_TMA_WARP) {
+    if (threadIdx.x == 32 * TMA_WARP) {
         prefetch_tensormap(&tq);
         prefetch_tensormap(&tk);
         prefetch_tensormap(&tv);
-        for (int b = 0; b < 2; b++) {
-            mbar_init(&sh.q_full[b], 1);
-            for (int x = 0; x < 2; x++) {
+        mbar_init(&sh.q_full, 1);
+        for (int b = 0; b < 2; b++)
+            for (int x = 0; x < CHAINS; x++) {
                 mbar_init(&sh.s_full[x][b], 1);
                 mbar_init(&sh.p_full[x][b], 4);
                 mbar_init(&sh.o_done[x][b], 1);
             }
-        }
-        for (int b = 0; b < MSK_SLOTS; b++) {
+        for (int b = 0; b < k_slots; b++) {
             mbar_init(&sh.k_full[b], 1);
-            mbar_init(&sh.k_empty[b], 2);  // both tiles' issuers
+            mbar_init(&sh.k_empty[b], CHAINS);
         }
-        for (int b = 0; b < MSK_V_SLOTS; b++) {
+        for (int b = 0; b < v_slots; b++) {
             mbar_init(&sh.v_full[b], 1);
             mbar_init(&sh.v_ready[b], 1);
-            mbar_init(&sh.v_empty[b], 2);
+            mbar_init(&sh.v_empty[b], CHAINS);
         }
-        mbar_init(&sh.fin, 2);
+        mbar_init(&sh.fin, CHAINS);
         fence_mbar_init();
     }
     pdl_trigger();
     pdl_wait();  // q, k, v and the intervals may come from the previous kernel on the stream
-    if (warp == MSK_TMA_WARP) {
+    if (warp == TMA_WARP) {
         // the queries at once, while the intervals are read
         __syncwarp();
-        for (int x = 0; x < ntiles; x++) {
-            if (lane == 0) mbar_arrive_expect_tx(&sh.q_full[x], (uint32_t)(a.gp * a.tq) * ATT_DH * 2);
-            __syncwarp();
-            att_tma_tile(sQ + x * ATT_TILE, &tq, h0, q0 + x * a.tq, &sh.q_full[x], lane);
-        }
+        if (lane == 0) mbar_arrive_expect_tx(&sh.q_full, (uint32_t)(a.gp * a.tq) * ATT_DH * 2);
+        __syncwarp();
+        att_tma_tile(sQ, &tq, h0, q0, &sh.q_full, lane);
     }
 
     // This thread's row (softmax warps): query, head, interval.
-    const int t = warp >> 2, quad = warp & 3, row = threadIdx.x & 127;
+    const int t = halves ? warp >> 2 : 0, quad = warp & 3, row = threadIdx.x & 127;
     int qi = 0, head = 0, lo = 0, hi = 0;
     bool live = false;
-    if (warp < MSK_SOFTMAX_WARPS) {
-        qi = q0 + (halves ? 0 : t) * a.tq + row / a.gp;
+    if (warp < MMA_WARP) {
+        qi = q0 + row / a.gp;
         head = h0 + row % a.gp;
-        live = (halves || t < ntiles) && row < a.tq * a.gp && qi < a.Lq;
+        live = row < a.tq * a.gp && qi < a.Lq;
         if (live) {
             lo = a.kv_begin ? max(0, __ldg(a.kv_begin + qi)) : 0;
             hi = a.kv_end ? min(a.Lk, __ldg(a.kv_end + qi)) : a.Lk;
@@ -264,42 +271,34 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
     tc_fence_after();
     const uint32_t tm = sh.tmem;
 
-    // Key blocks of each tile, and of the CTA's part of their union: [B0, B1).
-    int t0[2], t1[2], b_full0 = 0, b_full1 = INT_MAX;  // keys every row of the CTA sees
+    // Key blocks that any row of the CTA sees, and the CTA's part of them: [B0, B1).
+    int l0 = INT_MAX, h1 = 0, b_full0 = 0, b_full1 = INT_MAX;  // keys that every row sees
 #pragma unroll
-    for (int x = 0; x < 2; x++) {
-        int l = INT_MAX, h = 0;
-#pragma unroll
-        for (int w = 4 * x; w < 4 * x + 4; w++) {
-            l = min(l, sh.lo_min[w]);
-            h = max(h, sh.hi_max[w]);
-            b_full0 = max(b_full0, sh.lo_max[w]);
-            b_full1 = min(b_full1, sh.hi_min[w]);
-        }
-        t0[x] = l < h ? l / MSK_BK : 0;
-        t1[x] = l < h ? (h + MSK_BK - 1) / MSK_BK : 0;
+    for (int w = 0; w < 4; w++) {  // (halves: both chains have the same rows)
+        l0 = min(l0, sh.lo_min[w]);
+        h1 = max(h1, sh.hi_max[w]);
+        b_full0 = max(b_full0, sh.lo_max[w]);
+        b_full1 = min(b_full1, sh.hi_min[w]);
     }
-    int B0 = t0[0] < t1[0] ? (t0[1] < t1[1] ? min(t0[0], t0[1]) : t0[0]) : t0[1], B1 = max(t1[0], t1[1]);
+    int B0 = l0 < h1 ? l0 / MSK_BK : 0, B1 = l0 < h1 ? (h1 + MSK_BK - 1) / MSK_BK : 0;
     if (a.splits > 1) {
         const int n = (B1 - B0 + a.splits - 1) / a.splits;
         B0 = min(B1, B0 + (int)blockIdx.y * n);
         B1 = min(B1, B0 + n);
     }
-#pragma unroll
-    for (int x = 0; x < 2; x++) t0[x] = max(t0[x], B0), t1[x] = min(t1[x], B1);  // empty where t0 >= t1
-    const int N = max(0, B1 - B0), mid = B0 + (N + 1) / 2;
-    if (halves) t0[0] = B0, t1[0] = t0[1] = mid, t1[1] = B1;
-    // The n-th block that is loaded: in order, or from the halves in turn; and whether tile x
-    // works on it, as its block number i.
+    const int N = B1 - B0, mid = B0 + (N + 1) / 2;
+    // The blocks of each chain; the n-th block that is loaded: in order, or from the halves in
+    // turn; and whether chain x works on it, as its block number i.
+    const int t0[2] = {B0, halves ? mid : B1}, t1[2] = {halves ? mid : B1, B1};
     auto block = [&](int n) { return halves ? ((n & 1) ? mid : B0) + (n >> 1) : B0 + n; };
-    auto owns = [&](int x, int n) { return halves ? (n & 1) == x : B0 + n >= t0[x] && B0 + n < t1[x]; };
-    auto local = [&](int x, int n) { return halves ? n >> 1 : B0 + n - t0[x]; };
-    // A block that every row of both tiles sees whole needs no gate.
+    auto owns = [&](int x, int n) { return !halves || (n & 1) == x; };
+    auto local = [&](int x, int n) { return halves ? n >> 1 : n; };
+    // A block that every row sees whole needs no gate.
     auto whole = [&](int kb) { return kb * MSK_BK >= b_full0 && (kb + 1) * MSK_BK <= b_full1; };
 
-    if (warp >= MSK_SOFTMAX_WARPS) {
-        setmaxnreg_dec<MSK_REG_OTHER>();
-        if (warp == MSK_TMA_WARP) {
+    if (warp >= MMA_WARP) {
+        setmaxnreg_dec<msk_reg_other(halves)>();
+        if (warp == TMA_WARP) {
             // ------------------------------------------------------------ TMA producer
             int nk = 0, nv = 0;
             auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* full, int kb) {
@@ -307,27 +306,32 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
                 __syncwarp();
                 if (lane < 2) tma_load_3d(dst + lane * (MSK_KV / 2), map, 64 * lane, hk, kb * MSK_BK, full);
             };
+            // (slots as counters: three of them make no mask)
+            int b = 0, c = 0;
+            uint32_t kp = 1, vp = 1;  // parity of the slot's last release (first round: passes at once)
             for (int n = 0; n < N; n++) {
-                const int b = n % MSK_SLOTS, c = v_slot(n);
-                if (n >= MSK_SLOTS && !__all_sync(~0u, att_wait(&sh.k_empty[b], (n / MSK_SLOTS - 1) & 1))) break;
+                if (!__all_sync(~0u, att_wait(&sh.k_empty[b], kp))) break;
                 load(sK + b * MSK_KV, &tk, &sh.k_full[b], block(n));
                 nk = n + 1;
-                if (n >= v_slots && !__all_sync(~0u, att_wait(&sh.v_empty[c], v_use(n - v_slots)))) break;
+                if (++b == k_slots) b = 0, kp ^= 1;
+                if (!__all_sync(~0u, att_wait(&sh.v_empty[c], vp))) break;
                 load(sV + c * MSK_KV, &tv, &sh.v_full[c], block(n));
                 nv = n + 1;
+                if (++c == v_slots) c = 0, vp ^= 1;
             }
             // No copy may still be landing when the CTA exits, also when a wait ran out.
             if (lane == 0) {
-                for (int m = max(0, nk - MSK_SLOTS); m < nk; m++) drain_wait(&sh.k_full[m % MSK_SLOTS], (m / MSK_SLOTS) & 1);
-                for (int m = max(0, nv - v_slots); m < nv; m++) drain_wait(&sh.v_full[v_slot(m)], v_use(m));
-                for (int x = 0; x < ntiles; x++) drain_wait(&sh.q_full[x], 0);
+                for (int m = max(0, nk - k_slots); m < nk; m++) drain_wait(&sh.k_full[m % k_slots], (m / k_slots) & 1);
+                for (int m = max(0, nv - v_slots); m < nv; m++) drain_wait(&sh.v_full[m % v_slots], (m / v_slots) & 1);
+                drain_wait(&sh.q_full, 0);
             }
             __syncwarp();
-        } else if (warp == MSK_GATE_WARP) {
+        } else if (warp == GATE_WARP) {
             // ------------------------------------------------------------ V's gate
+            int b = 0;
+            uint32_t vp = 0;
             for (int n = 0; n < N; n++) {
-                const int b = v_slot(n);
-                if (!__all_sync(~0u, att_wait(&sh.v_full[b], v_use(n)))) break;
+                if (!__all_sync(~0u, att_wait(&sh.v_full[b], vp))) break;
                 if (!whole(block(n))) {
                     if (lane < 2) sh.flags[b][lane] = 0;
                     __syncwarp();
@@ -359,26 +363,29 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
                     __syncwarp();
                 }
                 if (lane == 0) mbar_arrive(&sh.v_ready[b]);
+                if (++b == v_slots) b = 0, vp ^= 1;
             }
-        } else {
-            // ------------------------------------------------------------ MMA issue, tile x
+        } else if (warp < MMA_WARP + CHAINS) {
+            // ------------------------------------------------------------ MMA issue, chain x
             constexpr uint32_t ID_S = idesc_f16(128, MSK_BK);
             constexpr uint32_t ID_O = idesc_f16(128, ATT_DH) | (1u << 16);  // B (V) MN-major
-            const int x = __shfl_sync(~0u, warp - MSK_MMA_WARP, 0);
+            const int x = __shfl_sync(~0u, warp - MMA_WARP, 0);
             const uint32_t el = elect_one();
             const uint32_t tO = tm + 256 * x, tS = tO + 128;
-            const int xq = halves ? 0 : x;  // whose queries
-            const uint64_t dq = att_qk_desc(sQ) + (uint64_t)(xq * (ATT_TILE >> 4)), dk = att_qk_desc(sK);
+            const uint64_t dq = att_qk_desc(sQ), dk = att_qk_desc(sK);
             const uint64_t dv = sdesc_sw128(smem_u32(sV), MSK_KV / 2, 1024);
             bool ok = true;
             auto wait = [&](uint64_t* bar, uint32_t parity) { ok = ok && __all_sync(~0u, att_wait(bar, parity)); };
             // S of the n-th block.  A block that is not the tile's is waited for all the same
             // before its slot is given back.
+            int kb = 0, vb = 0;
+            uint32_t kp = 0, vp = 0;
             auto scores = [&](int n) {
-                const int b = n % MSK_SLOTS;
+                const int b = kb;
                 if (n >= N) return;
-                wait(&sh.k_full[b], (n / MSK_SLOTS) & 1);
+                wait(&sh.k_full[b], kp);
                 if (!ok) return;
+                if (++kb == k_slots) kb = 0, kp ^= 1;
                 if (owns(x, n)) {
                     tc_fence_after();
                     const int sl = local(x, n) & 1;
@@ -392,15 +399,14 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
                 }
                 if (el) tc_commit(&sh.k_empty[b]);
             };
-            if (t0[0] < t1[0] || t0[1] < t1[1]) {
-                if (xq < ntiles) wait(&sh.q_full[xq], 0);
-            }
+            if (N > 0) wait(&sh.q_full, 0);
             const int ahead = halves ? 4 : 2;  // two of the tile's own blocks
 #pragma unroll 1
             for (int n = -ahead; ok && n < N; n++) {
                 if (n >= 0) {
-                    const int b = v_slot(n);
-                    wait(&sh.v_ready[b], v_use(n));
+                    const int b = vb;
+                    wait(&sh.v_ready[b], vp);
+                    if (++vb == v_slots) vb = 0, vp ^= 1;
                     if (owns(x, n)) {
                         const int i = local(x, n), sl = i & 1;
                         wait(&sh.p_full[x][sl], (i >> 1) & 1);
@@ -431,6 +437,7 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
         setmaxnreg_inc<MSK_REG_SOFTMAX>();
         const uint32_t tO = tm + ((uint32_t)(32 * quad) << 16) + 256 * t;
         const int kb0 = t ? t0[1] : t0[0], kb1 = t ? t1[1] : t1[0];
+        int vs = t, vp = 0;  // V slot of the present block and its parity
         const int w_lo0 = sh.lo_min[warp], w_hi1 = sh.hi_max[warp], w_lo1 = sh.lo_max[warp], w_hi0 = sh.hi_min[warp];
         const bool some = lo < hi;
         if (!some) lo = 0, hi = a.Lk;  // a row without keys runs along; it stores zeros
@@ -558,17 +565,18 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
             }
             if (!unseen && !whole(kb)) {  // V's gate: a marked key of the row's own?
                 // (before P is handed over: after that the slot may be refilled)
-                const int n = halves ? 2 * (kb - kb0) + t : kb - B0, b = v_slot(n);
-                if (!__all_sync(~0u, att_wait(&sh.v_ready[b], v_use(n)))) l = NAN;
+                if (!__all_sync(~0u, att_wait(&sh.v_ready[vs], vp))) l = NAN;
 #pragma unroll 1
                 for (int w = 0; w < 2; w++)
-                    for (uint32_t f = sh.flags[b][w]; f; f &= f - 1)
+                    for (uint32_t f = sh.flags[vs][w]; f; f &= f - 1)
                         if ((uint32_t)(k0 + 32 * w + __ffs(f) - 1 - lo) < (uint32_t)(hi - lo)) l = NAN;
             }
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.p_full[t][sl]);
+            vs += CHAINS;
+            if (vs >= v_slots) vs -= v_slots, vp ^= 1;
         }
         // The last P V of a tile with blocks.
         auto last = [&](int x) {
@@ -593,7 +601,7 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
         }
         const bool any = some && (ran || ran_x);
         // Without a block: the queries' copy must have landed before their space is used again.
-        if (!ran && !ran_x && (halves || t < ntiles)) ok = ok && __all_sync(~0u, att_wait(&sh.q_full[halves ? 0 : t], 0));
+        if (!ran && !ran_x) ok = ok && __all_sync(~0u, att_wait(&sh.q_full, 0));
         if (ok) {
             tc_fence_after();
             const int64_t at = (int64_t)qi * a.H + head;
@@ -604,7 +612,7 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
             fx *= inv;
             if (split && live && !(halves && t)) a.part_ml[pat] = any ? make_float2(m, l) : make_float2(-INFINITY, 0.0f);
             // 64 columns at a time (halves: one each) through shared memory (8 KB a warp of the
-            // queries' and, with one tile, the keys' space, which nothing reads any more), so that a store covers whole
+            // queries' and, with halves, the keys' space, which nothing reads any more), so that a store covers whole
             // lines: 32 rows of 16 bytes keep the store unit busy for 32 cycles.  Rows of 256
             // bytes, 16-byte chunk c of row i at c ^ (i & 15).  Small loops: this code runs once.
             const bool f32 = split || !a.o_f16;
@@ -661,9 +669,9 @@ __global__ void __launch_bounds__(MSK_THREADS, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == MSK_MMA_WARP) {
+    if (warp == MMA_WARP) {
         tc_fence_after();
-        tmem_dealloc(tm, ATT_TM_COLS);
+        tmem_dealloc(tm, 256 * CHAINS);
     }
 }
 

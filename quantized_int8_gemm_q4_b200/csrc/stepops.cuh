@@ -43,28 +43,24 @@ bool encode_rows(CUtensorMap* m, const void* base, int64_t rows, int64_t heads, 
 }
 
 struct MaskPlan {
-    int gp, tq, tiles, splits;
+    int gp, tq, splits;
+    bool halves;
     int64_t grid;
     size_t ml_off, bytes;
 };
 
-// Tiles, CTAs and key parts of a masked attention call.  Two query tiles per CTA once one
-// each would need more than one wave; with at most half a wave of CTAs the keys are cut
-// into parts of at least eight blocks, up to one wave in all.  Three waves of one tile take
-// ~1.7 times as long as one of two, and two waves of two tiles twice as long, as far as the
-// softmax's chain and not the loading of keys sets the pace: with a cap or a bias (long_chain;
-// 32 heads, 1200 positions, capped: all keys 70.7 -> 59.5 us, eight documents 31.7 -> 29.8;
-// without either 53.3 -> 51.3 and 24.5 -> 26.4).
-MaskPlan mask_plan(int64_t Lq, int64_t Lk, int64_t H, int64_t Hkv, bool long_chain, int sms) {
+// CTAs and key parts of a masked attention call.  Two CTAs share an SM once there are more tiles
+// than SMs; else each has an SM and two chains of blocks; with at most half a wave of those the
+// keys are cut into parts of at least eight blocks, up to one wave in all.
+MaskPlan mask_plan(int64_t Lq, int64_t Lk, int64_t H, int64_t Hkv, int sms) {
     MaskPlan p;
     const int group = (int)(H / Hkv);
     p.gp = group < 128 ? group : 128;
     while (group % p.gp) p.gp--;
     p.tq = 128 / p.gp;
     const int64_t n_heads = H / p.gp, n_tiles = (Lq + p.tq - 1) / p.tq, blocks = (Lk + MSK_BK - 1) / MSK_BK;
-    const int64_t waves = (n_tiles * n_heads + sms - 1) / sms;
-    p.tiles = waves == 1 || (waves == 3 && long_chain) ? 1 : 2;
-    p.grid = (n_tiles + p.tiles - 1) / p.tiles * n_heads;
+    p.grid = n_tiles * n_heads;
+    p.halves = p.grid <= sms;
     p.splits = 1;
     if (2 * p.grid <= sms && blocks >= 16) {
         const int64_t most = sms / p.grid;
@@ -88,7 +84,7 @@ bool mask_attribute() {
     return cudaFuncSetAttribute(attention_masked_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)msk_smem(MODE & 4)) == cudaSuccess &&
            cudaFuncGetAttributes(&fa, attention_masked_kernel<MODE>) == cudaSuccess &&
-           fa.numRegs >= MSK_REG_LAUNCH;  // the warpgroups' setmaxnreg split must fit in the launch's registers
+           fa.numRegs >= msk_reg_launch(MODE & 4);  // the warpgroups' setmaxnreg split must fit in the launch's registers
 }
 
 bool mask_attributes(int dev) {
@@ -193,7 +189,7 @@ int dllm_attention_masked_workspace_bytes(int64_t Lq, int64_t Lk, int64_t H, int
     int dev;
     int rc = current_device(&dev);
     if (rc) return rc;
-    *bytes = mask_plan(Lq, Lk, H, Hkv, false, g_num_sms[dev]).bytes;
+    *bytes = mask_plan(Lq, Lk, H, Hkv, g_num_sms[dev]).bytes;
     return DLLM_OK;
 }
 
@@ -220,7 +216,7 @@ int dllm_attention_masked(const void* q, int64_t ldq, const void* k, int64_t ldk
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (Lk == 0)
         return status_of(cudaMemsetAsync(o, 0, (size_t)(Lq * H * dh) * (o_type == DLLM_F16 ? 2 : 4), s));
-    const MaskPlan p = mask_plan(Lq, Lk, H, Hkv, softcap > 0.0f || slopes, g_num_sms[dev]);
+    const MaskPlan p = mask_plan(Lq, Lk, H, Hkv, g_num_sms[dev]);
     if (p.grid > (1LL << 31) - 1) return DLLM_ERR_ARG;
     if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes)) return DLLM_ERR_WORKSPACE;
     if (!mask_attributes(dev)) return DLLM_ERR_CUDA;
@@ -245,8 +241,8 @@ int dllm_attention_masked(const void* q, int64_t ldq, const void* k, int64_t ldk
     static const MaskKernel kernels[8] = {attention_masked_kernel<0>, attention_masked_kernel<1>, attention_masked_kernel<2>,
                                           attention_masked_kernel<3>, attention_masked_kernel<4>, attention_masked_kernel<5>,
                                           attention_masked_kernel<6>, attention_masked_kernel<7>};
-    const MaskKernel kernel = kernels[(softcap > 0.0f ? 1 : 0) + (slopes ? 2 : 0) + (p.tiles == 1 ? 4 : 0)];
-    rc = status_of(launch_pdl(kernel, grid, dim3(MSK_THREADS), msk_smem(p.tiles == 1), s, tq, tk, tv, a));
+    const MaskKernel kernel = kernels[(softcap > 0.0f ? 1 : 0) + (slopes ? 2 : 0) + (p.halves ? 4 : 0)];
+    rc = status_of(launch_pdl(kernel, grid, dim3(msk_threads(p.halves)), msk_smem(p.halves), s, tq, tk, tv, a));
     if (rc || p.splits == 1) return rc;
     return status_of(launch_pdl(attention_masked_join_kernel, dim3((unsigned)((Lq * H + 3) / 4)), dim3(128), 0, s, a.part,
                                 a.part_ml, Lq * H, p.splits, o, a.o_f16));
