@@ -40,7 +40,7 @@
 
 #include <cfloat>
 
-#include "layout.cuh"
+#include "attention.cuh"
 
 namespace dllm {
 
@@ -310,19 +310,29 @@ struct SampleRow {
             }
         });
         __syncthreads();
-        for (int cb = w; cb < SMP_COARSE; cb += SMP_WARPS) {
-            const int b = 32 * cb + lane;
-            const uint32_t c = __reduce_add_sync(0xffffffffu, sm.cnt[b]);
-            u64 m = 0;
+        // Coarse sums: eight bins per thread, four threads' together, written by those into every CTA.
+        static_assert(SMP_BINS == 8 * SMP_THREADS, "bins per thread");
+        uint32_t c = 0;
+        u64 m = 0;
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            const int b = 8 * (int)threadIdx.x + 4 * h;
+            const uint4 y = *reinterpret_cast<const uint4*>(&sm.cnt[b]);
+            c += (y.x + y.y) + (y.z + y.w);
             if (mass) {
-                const uint32_t x = sm.lo[b];
-                m = ((u64)__reduce_add_sync(0xffffffffu, sm.hi[b]) << 32) +
-                    ((u64)__reduce_add_sync(0xffffffffu, x >> 16) << 16) + __reduce_add_sync(0xffffffffu, x & 0xffffu);
+                const uint4 a = *reinterpret_cast<const uint4*>(&sm.lo[b]), d = *reinterpret_cast<const uint4*>(&sm.hi[b]);
+                m += ((u64)((d.x + d.y) + (d.z + d.w)) << 32) + (((u64)a.x + a.y) + ((u64)a.z + a.w));
             }
-            if (lane < C) {
-                *cl.map_shared_rank(&sm.ccnt[r][cb], lane) = c;
-                *cl.map_shared_rank(&sm.cmass[r][cb], lane) = m;
-            }
+        }
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+            c += __shfl_xor_sync(0xffffffffu, c, o);
+            m += __shfl_xor_sync(0xffffffffu, m, o);
+        }
+        for (int t = lane & 3; t < C; t += 4) {
+            const int cb = (int)threadIdx.x >> 2;
+            *cl.map_shared_rank(&sm.ccnt[r][cb], t) = c;
+            *cl.map_shared_rank(&sm.cmass[r][cb], t) = m;
         }
         cl.sync();
         if (w == 0) {
@@ -499,7 +509,7 @@ __global__ void __launch_bounds__(SMP_THREADS, 2) sample_kernel(const __grid_con
 #pragma unroll
             for (int j = 0; j < 4; j++) {
                 const float z = fmaxf(l[j] - top, -200.0f);  // e^-200 is 0 in f32
-                const float e = z < 0.0f ? exp2f(z * 1.4426950408889634f) : 0.0f;
+                const float e = z < 0.0f ? att_ex2(z * 1.4426950408889634f) : 0.0f;
                 eq += z == 0.0f;
                 e1 += e;
                 e2 = fmaf(e, z, e2);
@@ -583,33 +593,50 @@ __global__ void __launch_bounds__(SMP_THREADS, 2) sample_kernel(const __grid_con
                     upto = (uint32_t)min(candidates, (u64)0xffffffffu);
                     if (all && upto > SMP_LIST) break;
                 }
+                if (w == 0) {
+                    if (!all) row.cross(by_count, limit);
+                    if (lane == 0) sm.best = 0, sm.n_mine[half] = 0;
+                }
+                __syncthreads();
                 if (!all) {
-                    if (w == 0) {
-                        row.cross(by_count, limit);
-                        if (lane == 0) sm.best = 0, sm.n_mine[half] = 0;
-                    }
-                    __syncthreads();
                     bin = (int)sm.found_bin;
                     upto = sm.found_upto;
                     c0 = sm.found[0];
                     m0 = sm.found[1];
                 }
+                // The bin's edges, with a hundredth of a bin for the rounding of bin_of and a
+                // few units in the last place for their own; the last bin reaches down.
+                const float slack = 4e-6f * fabsf(row.vhi);
+                const float under = !row.linear               ? row.vmin
+                                    : bin == SMP_BINS - 1 ? -INFINITY
+                                                          : 4.0f * (row.vhi - ((float)bin + 0.51f) / row.inv) - slack;
                 if (whole && upto <= SMP_LIST) {
                     // Few candidates up to the end of the crossing bin (any cut of an earlier
-                    // stage included): CTA 0 ranks them all and takes the token from them.
+                    // stage included): CTA 0 ranks them all and takes the token from them.  They
+                    // are gathered here first, so that each CTA asks for its place once.
+                    const float least = fmaxf(row.low_val, under);
                     row.each(0, n, threadIdx.x, SMP_THREADS, [&](const float4& x, int i) {
                         const float l[4] = {x.x, x.y, x.z, x.w};
-                        if (!(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])) >= row.low_val)) return;
+                        if (!(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])) >= least)) return;
 #pragma unroll
                         for (int e = 0; e < 4; e++)
-                            if (row.in_range(l[e], i + e) && row.kept(l[e], i + e) && row.bin_of(l[e]) <= bin) {
+                            if (l[e] >= least && row.in_range(l[e], i + e) && row.kept(l[e], i + e) && row.bin_of(l[e]) <= bin) {
                                 if (mass && row.weight1(l[e]) == 0) continue;
-                                SampleShared* o = cl.map_shared_rank(&sm, 0);
-                                const uint32_t slot = atomicAdd(&o->n_list, 1u);
+                                const uint32_t slot = atomicAdd(&sm.n_mine[half], 1u);
                                 if (slot < SMP_LIST)
-                                    o->list[slot].x = ((u64)smp_key(l[e]) << 32) | (uint32_t)~row.index(i + e);
+                                    sm.mine[half][slot] = ((u64)smp_key(l[e]) << 32) | (uint32_t)~row.index(i + e);
                             }
                     });
+                    __syncthreads();
+                    const uint32_t count = min(sm.n_mine[half], (uint32_t)SMP_LIST);
+                    if (w * 32 < (int)count) {
+                        SampleShared* o = cl.map_shared_rank(&sm, 0);
+                        const uint32_t of_warp = min(count - 32 * w, 32u);
+                        uint32_t slot = 0;
+                        if (lane == 0) slot = atomicAdd(&o->n_list, of_warp);
+                        slot = __shfl_sync(0xffffffffu, slot, 0) + lane;
+                        if (lane < (int)of_warp && slot < SMP_LIST) o->list[slot].x = sm.mine[half][threadIdx.x];
+                    }
                     cl.sync();
                     if (r != 0) return;  // nothing of this CTA's memory is read from here on
                     const int m = (int)min(sm.n_list, (uint32_t)SMP_LIST), e = (int)threadIdx.x;
@@ -660,12 +687,6 @@ __global__ void __launch_bounds__(SMP_THREADS, 2) sample_kernel(const __grid_con
                     }
                     return;
                 }
-                // The bin's edges, with a hundredth of a bin for the rounding of bin_of and a
-                // few units in the last place for their own; the last bin reaches down.
-                const float slack = 4e-6f * fabsf(row.vhi);
-                const float under = !row.linear               ? row.vmin
-                                    : bin == SMP_BINS - 1 ? -INFINITY
-                                                          : 4.0f * (row.vhi - ((float)bin + 0.51f) / row.inv) - slack;
                 const float over = row.linear ? 4.0f * (row.vhi - ((float)bin - 0.51f) / row.inv) + slack : row.vmax;
                 uint32_t k_hi = 0, k_lo = 0;  // largest code of the bin, largest complement
                 row.each(0, n, threadIdx.x, SMP_THREADS, [&](const float4& x, int i) {
