@@ -98,6 +98,13 @@ __device__ __forceinline__ float smp_value(uint32_t k) {
     return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
 
+// The largest of three; NaN if one is.
+__device__ __forceinline__ float smp_max3(float a, float b, float c) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 __device__ __forceinline__ u64 smp_warp_sum(u64 v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -290,10 +297,10 @@ struct SampleRow {
         }
         each(0, n, threadIdx.x, SMP_THREADS, [&](const float4& x, int i) {
             const float l[4] = {x.x, x.y, x.z, x.w};
+            if (!(fmaxf(max3f(l[0], l[1], l[2]), l[3]) >= low_val)) return;
             bool ok[4];
 #pragma unroll
             for (int e = 0; e < 4; e++) ok[e] = uncut ? l[e] >= lo : in_range(l[e], i + e);
-            if (!(ok[0] | ok[1] | ok[2] | ok[3])) return;
             u64 v[4];
             if (mass) weight4(l, ok, v);
 #pragma unroll
@@ -456,13 +463,11 @@ __global__ void __launch_bounds__(SMP_THREADS, 2) sample_kernel(const __grid_con
     float hi = -INFINITY, lo = INFINITY;
     row.each(0, n, threadIdx.x, SMP_THREADS, [&](const float4& x, int) {
         const float xs[4] = {x.x, x.y, x.z, x.w};
+        hi = smp_max3(smp_max3(hi, x.x, x.y), x.z, x.w);
 #pragma unroll
-        for (int e = 0; e < 4; e++) {
-            bad |= !(xs[e] < INFINITY);  // +inf or NaN
-            hi = fmaxf(hi, xs[e]);
-            lo = fminf(lo, xs[e] > -INFINITY ? xs[e] : INFINITY);
-        }
+        for (int e = 0; e < 4; e++) lo = fminf(lo, xs[e] > -INFINITY ? xs[e] : INFINITY);
     });
+    bad |= !(hi < INFINITY);  // +inf or NaN
     uint32_t m1 = __reduce_max_sync(0xffffffffu, smp_key(hi)), m2 = __reduce_max_sync(0xffffffffu, ~smp_key(lo));
     uint32_t m3 = __any_sync(0xffffffffu, bad);
     if (lane == 0) sm.red[0][w] = m1, sm.red[1][w] = m2, sm.red[2][w] = m3;
