@@ -25,16 +25,18 @@
 // the 32 bins behind the crossing one are then read from the other CTAs.
 // Few candidates (up to 256 up to the end of a limit's bin, as min_p, top_k and peaked rows leave)
 // are gathered in one CTA, which ranks them and takes the token from them.
-// Bound: the logits' bytes; in practice the chain of passes and barriers (~38,000 cycles per
+// Bound: the logits' bytes; in practice the chain of passes and barriers (~26,000 cycles per
 // CTA where few candidates are left, two CTAs per SM) and, for flat rows, the weights: ~40
-// instructions an element, a third of them f64, and two to three shared-memory atomics of 4-5
-// cycles each.
+// instructions an element, a third of them f64, on pipes that take one every other cycle, and two
+// to three shared-memory atomics of 4-5 cycles each.
 //
-// Measured (one B200): 1 row of 152064 words with all limits 14.2 us; 32 rows of 126464 with top_p
-// 60 us; 256 rows with all limits 158 us (0.82 TB/s).  Steps on the way: f64 exponentials of the math
+// Measured (one B200): 1 row of 152064 words with all limits 11.3 us; 32 rows of 126464 with top_p
+// 51 us; 256 rows with all limits 126 us (1.03 TB/s).  Steps on the way: f64 exponentials of the math
 // library, a histogram per limit, 1024 threads 60 / 139 / 934 us; one histogram for both limits,
 // two CTAs per SM 39 / 79 / 385; weights by table 22 / 52 / 221; bulk copies and the list of few
-// candidates 15.5 / 62 / 177; 256 threads at 128 registers 14.4 / 60 / 158.
+// candidates 15.5 / 62 / 177; 256 threads at 128 registers 14.4 / 60 / 158; coarse sums by vector
+// loads, lists gathered per CTA 12.0 / 55 / 137; vectors passed over whole 11.1 / 57 / 124; bins of
+// top_p alone no lower than its cut can be 11.3 / 51 / 126.
 #pragma once
 #include <cooperative_groups.h>
 
@@ -279,22 +281,26 @@ struct SampleRow {
     // sums before each coarse bin, starting from c0, m0.  by_value spreads the values evenly
     // over the bins (both sides scaled by 1/4, so that no difference overflows; monotone, as
     // each operation rounds monotonically); else the codes, which always splits the range.
-    __device__ __forceinline__ void histogram(float lo, float hi, bool by_value, bool clear, bool mass, u64 c0, u64 m0) {
+    // By value and with masses the bins may begin at `bins`, above lo: the last has all from lo to there.
+    __device__ __forceinline__ void histogram(float lo, float hi, float bins, bool by_value, bool clear, bool mass, u64 c0, u64 m0) {
         SampleShared& sm = smp_shared();
         vmin = lo;
         vmax = hi;
         low_val = fmaxf(lo, cut_val);
         low_i = lo > cut_val ? INT_MAX : cut_i;
         vhi = 0.25f * hi;
-        const float span = vhi - 0.25f * lo;
+        const float span = vhi - 0.25f * bins;
         inv = (float)SMP_BINS / span;
         shift = max(0, 32 - __clz(smp_key(hi) - smp_key(lo)) - 11);
         linear = by_value && span > 0.0f && inv < 1e30f;
+        if (!linear) bins = lo;
         const bool uncut = by_value && low_i == INT_MAX;  // every value from lo up is a candidate
         if (clear) {
             for (int i = threadIdx.x; i < SMP_BINS; i += SMP_THREADS) sm.cnt[i] = sm.lo[i] = sm.hi[i] = 0;
             __syncthreads();
         }
+        u64 below = 0;  // mass and number of what lies below the bins: summed here, not by atomics on one bin
+        uint32_t n_below = 0;
         each(0, n, threadIdx.x, SMP_THREADS, [&](const float4& x, int i) {
             const float l[4] = {x.x, x.y, x.z, x.w};
             if (!(fmaxf(max3f(l[0], l[1], l[2]), l[3]) >= low_val)) return;
@@ -302,11 +308,17 @@ struct SampleRow {
 #pragma unroll
             for (int e = 0; e < 4; e++) ok[e] = uncut ? l[e] >= lo : in_range(l[e], i + e);
             u64 v[4];
-            if (mass) weight4(l, ok, v);
+            const bool any4[4] = {true, true, true, true};  // what is not ok is left out below
+            if (mass) weight4(l, any4, v);
 #pragma unroll
             for (int e = 0; e < 4; e++) {
                 // a weight of 0: no candidate, or one that no mass limit can tell apart
                 if (!ok[e] || (mass && v[e] == 0)) continue;
+                if (l[e] < bins) {
+                    below += v[e];
+                    n_below++;
+                    continue;
+                }
                 const int b = bin_of(l[e]);
                 if (mass) {  // two 32-bit adds: a 64-bit one is a compare-and-swap loop
                     const uint32_t wl = (uint32_t)v[e], old = atomicAdd(&sm.lo[b], wl);
@@ -316,6 +328,15 @@ struct SampleRow {
                 atomicAdd(&sm.cnt[b], 1u);
             }
         });
+        if (bins > lo) {  // uniform
+            below = smp_warp_sum(below);
+            n_below = __reduce_add_sync(0xffffffffu, n_below);
+            if (lane == 0 && n_below) {
+                const uint32_t bl = (uint32_t)below, old = atomicAdd(&sm.lo[SMP_BINS - 1], bl);
+                atomicAdd(&sm.hi[SMP_BINS - 1], (uint32_t)(below >> 32) + (old + bl < old ? 1u : 0u));
+                atomicAdd(&sm.cnt[SMP_BINS - 1], n_below);
+            }
+        }
         __syncthreads();
         // Coarse sums: eight bins per thread, four threads' together, written by those into every CTA.
         static_assert(SMP_BINS == 8 * SMP_THREADS, "bins per thread");
@@ -574,11 +595,17 @@ __global__ void __launch_bounds__(SMP_THREADS, 2) sample_kernel(const __grid_con
                 if (min_p > 0.0)
                     from = fmaxf(from, __double2float_rd((double)top - (-sm.ln_min_p * 1.000001 + 1e-12) * Td - hair));
             }
+            // The cut and what follows it hold more than (1 - p) of the mass, which is at least the
+            // largest weight, 1, and none of them weighs more than the cut: it weighs more than
+            // (1 - p) / V, so the bins need not reach below that (with some room for rounding).
+            float bins = from;
+            if (!by_count && k <= 0 && p > 0.0f)
+                bins = fmaxf(from, __double2float_rd((double)top + (log((1.0 - (double)p) / (double)a.V) - 0.01) * Td - hair));
             u64 c0 = 0, m0 = 0, limit = 0;
             bool whole = true, done = false;
 #pragma unroll 1
             while (!done) {
-                if (!have) row.histogram(from, to, whole, clear, mass, c0, m0);
+                if (!have) row.histogram(from, to, whole ? bins : from, whole, clear, mass, c0, m0);
                 have = clear = true;
                 int bin = SMP_BINS - 1;
                 uint32_t upto = 0;

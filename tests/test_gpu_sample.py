@@ -122,6 +122,21 @@ def test_each_limit_alone(limit, V):
           p=g.uniform(0.01, 1.0, R) if limit == "p" else None, mp=g.uniform(0, 1, R) if limit == "mp" else None, u=u)
 
 
+@pytest.mark.parametrize("spread", [0.01, 1.0, 4.0, 30.0])
+@pytest.mark.parametrize("V", [1, 7, 5000, 126464])
+def test_top_p_alone_from_one_word_to_nearly_all(V, spread):
+    """The cut in the first bin, in the middle, and far down the tail, behind words that no bin holds."""
+    p = np.array([2.0 ** -24, 0.01, 0.5, 0.9, 0.99, 0.9999, 1 - 2.0 ** -20, 1 - 2.0 ** -24], np.float32)
+    R = len(p)
+    x, g = logits_of(R, V, 10, spread)
+    u = g.uniform(0, 1, R)
+    for T in (0.2, 1.0, 5.0):
+        check(x, T=np.full(R, T), p=p, u=u)
+    check(np.round(x), p=p, u=u)
+    x[:, 1::3] = -np.inf
+    check(x, T=np.full(R, 0.8), p=p, u=u)
+
+
 def test_ties_go_to_the_lowest_index():
     """Equal logits at the border of a limit: more than the ranked list holds, and fewer."""
     R, V = 8, 20000
