@@ -65,6 +65,13 @@ MaskPlan mask_plan(int64_t Lq, int64_t Lk, int64_t H, int64_t Hkv, int sms) {
     if (2 * p.grid <= sms && blocks >= 16) {
         const int64_t most = sms / p.grid;
         p.splits = (int)(most < blocks / 8 ? most : blocks / 8);
+        // One part per SM leaves a tenth of the SMs or more without work (32 heads on 148 SMs: 20): two
+        // CTAs per SM in parts of half the length leave fewer, for parts long enough that streaming
+        // the keys is all that counts (one query over 20011 keys 58.8 -> 57.0 us, over 60000
+        // 157.6 -> 147.1; 8 tiles, which leave 4 SMs idle, 49.4 -> 54.6 over 60000).
+        const int64_t more = 2 * sms / p.grid;
+        if (10 * (sms - most * p.grid) >= sms && more > 2 * most && more <= blocks / 32)
+            p.halves = false, p.splits = (int)more;
     }
     p.ml_off = p.bytes = 0;
     if (p.splits > 1) {

@@ -293,6 +293,22 @@ def test_holes_in_a_long_prefix():
         check(q, k, v, b, e)
 
 
+@pytest.mark.parametrize("H,Lk", [(32, 19000), (55, 10500)])
+def test_long_caches_of_many_heads(H, Lk):
+    """Key parts of half an SM each: whole intervals, a stretch in one part, one across several, none."""
+    q, k, v = inputs(4, Lk, H, H, 25)
+    check(q, k, v)
+    b, e = t([Lk - 9, 3000, 17, 50]), t([Lk, 9001, 20, 50])
+    slopes = torch.rand(H, device="cuda") * 0.01
+    check(q, k, v, b, e)
+    check(q, k, v, b, e, cap=20.0, slopes=slopes, qp=t([Lk, 5000, 0, 7]))
+    k[9001:Lk - 9], v[9001:Lk - 9] = float("nan"), INF
+    check(q, k, v, b, e)
+    v[8000, :, 5] = float("nan")  # attended by the second query only
+    o = call(q, k, v, Lk, b, e)[:4].float()
+    assert not bool(torch.isfinite(o[1, :, 5]).any()) and bool(torch.isfinite(o[[0, 2, 3]]).all())
+
+
 def test_rows_in_a_fused_buffer_and_a_longer_cache():
     L, H, Hkv = 150, 6, 2
     buf = torch.randn(L, (H + 2 * Hkv) * DH + 64, device="cuda").half()
