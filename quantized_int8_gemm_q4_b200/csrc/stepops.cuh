@@ -51,7 +51,7 @@ struct MaskPlan {
 
 // CTAs and key parts of a masked attention call.  Two CTAs share an SM once there are more tiles
 // than SMs; else each has an SM and two chains of blocks; with at most half a wave of those the
-// keys are cut into parts of at least eight blocks, up to one wave in all.
+// keys are cut into parts, up to one wave in all.
 MaskPlan mask_plan(int64_t Lq, int64_t Lk, int64_t H, int64_t Hkv, int sms) {
     MaskPlan p;
     const int group = (int)(H / Hkv);
@@ -62,9 +62,14 @@ MaskPlan mask_plan(int64_t Lq, int64_t Lk, int64_t H, int64_t Hkv, int sms) {
     p.grid = n_tiles * n_heads;
     p.halves = p.grid <= sms;
     p.splits = 1;
-    if (2 * p.grid <= sms && blocks >= 16) {
+    if (2 * p.grid <= sms && blocks >= 12) {
+        // n parts take ~0.45 us blocks / n for their chains and 0.18 us n for the join, least at
+        // n^2 = 2.5 blocks (one query of 28 heads on 4: 1000 keys 2 parts 11.9 us, 5 10.1; 8200 keys
+        // 16 parts 16.9, 32 18.0)
         const int64_t most = sms / p.grid;
-        p.splits = (int)(most < blocks / 8 ? most : blocks / 8);
+        int64_t n = most < blocks / 3 ? most : blocks / 3;
+        while (2 * n * n > 5 * blocks) n--;
+        p.splits = (int)n;
         // One part per SM leaves a tenth of the SMs or more without work (32 heads on 148 SMs: 20): two
         // CTAs per SM in parts of half the length leave fewer, for parts long enough that streaming
         // the keys is all that counts (one query over 20011 keys 58.8 -> 57.0 us, over 60000
