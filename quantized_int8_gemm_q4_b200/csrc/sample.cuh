@@ -841,7 +841,7 @@ __global__ void __launch_bounds__(SMP_THREADS, 2) sample_kernel(const __grid_con
         if (target >= before && target - before < mine) {  // in this CTA's slice (uniform)
             u64 run = before;
             int wi = 0;
-            while (run + sm.red[0][wi] <= target) run += sm.red[0][wi++];
+            while (wi < SMP_WARPS - 1 && run + sm.red[0][wi] <= target) run += sm.red[0][wi++];
             const int from = min(n, wi * per), to = min(n, from + per);
             for (int i0 = from; i0 < to; i0 += 4 * SMP_THREADS) {
                 const int i = i0 + 4 * (int)threadIdx.x;
