@@ -42,8 +42,8 @@
 // load, maximum, exponentials, store, hand-over) takes ~1900 cycles per block, and the two chains of
 // an SM run side by side: ~2000 cycles per block of both.
 //
-// Measured (one B200): 4096 positions under a 1000-position prefix, 32 heads: 156 us at 1965 MHz, 182 us
-// once the power cap holds the clock at 1680 MHz (800 TFLOP/s of attended pairs); six packed
+// Measured (one B200): 4096 positions under a 1000-position prefix, 32 heads: 154 us at 1965 MHz, 177 us
+// once the power cap holds the clock at 1680 MHz (820 TFLOP/s of attended pairs); six packed
 // documents over 1024 positions 16.3 us; one query over 20011 keys of 32 heads 58 us (5.7 TB/s);
 // 32 queries over 8200 keys, 28 heads on 4, 19.4 us; capped and biased, 1531 positions in three
 // documents, 39 us.
