@@ -72,7 +72,13 @@ struct SampleArgs {
 };
 
 struct alignas(16) SampleShared {  // the slice follows it, read in 16-byte vectors
-    ulonglong2 list[SMP_LIST];                           // all CTAs' elements of a gathered bin: order code, weight
+    // All CTAs' elements of a gathered bin, order code and weight.  This CTA alone writes it, and may still
+    // rank one limit's bin in it while another CTA has gone on to the next limit.
+    ulonglong2 list[SMP_LIST];
+    // CTA 0's: the order codes of few candidates, written once per row by every CTA that has some, and read
+    // behind the cluster barrier that follows.  Not `list`: no barrier lies between the ranking of top_k's
+    // bin and these writes.
+    u64 sent[SMP_LIST];
     uint32_t cnt[SMP_BINS], lo[SMP_BINS], hi[SMP_BINS];  // this CTA's histogram: count, mass
     uint32_t ccnt[SMP_MAX_CLUSTER][SMP_COARSE];          // every CTA's coarse sums
     u64 cmass[SMP_MAX_CLUSTER][SMP_COARSE];
@@ -667,15 +673,15 @@ __global__ void __launch_bounds__(SMP_THREADS, 2) sample_kernel(const __grid_con
                         uint32_t slot = 0;
                         if (lane == 0) slot = atomicAdd(&o->n_list, of_warp);
                         slot = __shfl_sync(0xffffffffu, slot, 0) + lane;
-                        if (lane < (int)of_warp && slot < SMP_LIST) o->list[slot].x = sm.mine[half][threadIdx.x];
+                        if (lane < (int)of_warp && slot < SMP_LIST) o->sent[slot] = sm.mine[half][threadIdx.x];
                     }
                     cl.sync();
                     if (r != 0) return;  // nothing of this CTA's memory is read from here on
                     const int m = (int)min(sm.n_list, (uint32_t)SMP_LIST), e = (int)threadIdx.x;
-                    const u64 code = e < m ? sm.list[e].x : 0;
+                    const u64 code = e < m ? sm.sent[e] : 0;
                     const float l = smp_value((uint32_t)(code >> 32));
                     u64 weight = e < m ? row.weight1(l) : 0;
-                    if (e < m) sm.list[e].y = weight;
+                    if (e < m) sm.list[e].x = code, sm.list[e].y = weight;
                     __syncthreads();
                     uint32_t rank = 0;
                     u64 pre = 0;

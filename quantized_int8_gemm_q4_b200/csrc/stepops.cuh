@@ -308,8 +308,8 @@ int dllm_sample(const float* logits, int64_t R, int64_t V, int64_t ldl, const fl
     if (C == 8 && 16 * R <= g_num_sms[dev] && g_sample_cluster16[dev]) C = 16;
     a.slice = (int32_t)round_up((V + 3 + C - 1) / C, 128);
     // Two CTAs per SM where at least 3/4 of a slice then fits in shared memory (the rest is
-    // read again from L2), else one.
-    const int64_t pair = (int64_t)((112 * 1024 - sizeof(SampleShared)) / 16 * 4);
+    // read again from L2), else one.  113 KB and the system's 1 KB per CTA twice are an SM's 228 KB.
+    const int64_t pair = (int64_t)((113 * 1024 - sizeof(SampleShared)) / 16 * 4);
     const int64_t room = 4 * pair >= 3 * (int64_t)a.slice ? pair : (int64_t)((most - sizeof(SampleShared)) / 16 * 4);
     a.cached = (int32_t)(a.slice < room ? a.slice : room);
     int bits = 0;
