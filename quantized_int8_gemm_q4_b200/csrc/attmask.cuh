@@ -55,6 +55,8 @@
 // exponential in four by polynomial (no gain) or in two (10% slower); all commits after the MMAs
 // (slots return later: one over 20011 66 -> 72 us).
 #pragma once
+#include <cfloat>
+
 #include "attention.cuh"
 #include "qgemm.cuh"
 #include "rope.cuh"
@@ -103,7 +105,7 @@ struct MaskArgs {
     void* o;
     int32_t o_f16;
     float* part;      // splits > 1: unnormalised O [splits][Lq][H][128]
-    float2* part_ml;  // and (m, l) [splits][Lq][H]
+    float2* part_ml;  // and (m, l) [splits][Lq][H]; m = -inf: no key of the row in this part
 };
 
 __device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
@@ -610,7 +612,12 @@ __global__ void __launch_bounds__(msk_threads(MODE & 4), MODE & 4 ? 1 : 2)
             const float inv = split ? 1.0f : 1.0f / l;
             f *= inv;
             fx *= inv;
-            if (split && live && !(halves && t)) a.part_ml[pat] = any ? make_float2(m, l) : make_float2(-INFINITY, 0.0f);
+            if (split && live && !(halves && t)) {
+                // m = -inf says that the row has no key here.  With keys whose scores are all NaN or -inf the
+                // lowest float stands for it: the join then takes the part's l and O, whose NaN the row gets.
+                const bool keys = any && lo < B1 * MSK_BK && hi > B0 * MSK_BK;
+                a.part_ml[pat] = keys ? make_float2(fmaxf(m, -FLT_MAX), l) : make_float2(-INFINITY, 0.0f);
+            }
             // 64 columns at a time (halves: one each) through shared memory (8 KB a warp of the
             // queries' and, with halves, the keys' space, which nothing reads any more), so that a store covers whole
             // lines: 32 rows of 16 bytes keep the store unit busy for 32 cycles.  Rows of 256
@@ -676,7 +683,8 @@ __global__ void __launch_bounds__(msk_threads(MODE & 4), MODE & 4 ? 1 : 2)
 }
 
 // Joins the parts of the key range: o = sum_z 2^(m_z - M) O_z / sum_z 2^(m_z - M) l_z, one
-// warp per (query, head); no key at all (every m -inf) gives zeros.
+// warp per (query, head); no key at all (every m -inf) gives zeros, keys without a finite score NaN
+// (a part with keys has a finite m or +inf, see MaskArgs).
 __global__ void __launch_bounds__(128) attention_masked_join_kernel(const float* __restrict__ part,
                                                                     const float2* __restrict__ ml, int64_t rows,
                                                                     int splits, void* __restrict__ o, int o_f16) {

@@ -1,0 +1,80 @@
+"""dllm_attention_masked on values that are not finite where a query does attend: what comes out does
+not depend on how the keys are split, nor on what the rows beside it see."""
+import numpy as np
+import pytest
+import torch
+
+from quantized_int8_gemm_q4_b200 import dllm
+from tests import test_gpu_attention_masked as att
+
+pytestmark = pytest.mark.gpu
+NAN, INF = float("nan"), float("inf")
+# (Lq, Lk, H, Hkv): keys split over CTAs, one query and a few, two CTAs per SM; halves; more tiles than SMs
+SHAPES = [(1, 3000, 4, 4), (5, 8200, 28, 4), (1, 19000, 32, 32), (3, 300, 4, 2), (200, 900, 4, 4), (300, 500, 64, 8)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU test run without a CUDA device")
+    from quantized_int8_gemm_q4_b200 import build
+    build.build()
+    dllm.load()
+    yield
+    assert dllm.dllm_get_device_status() == dllm.DLLM_OK
+
+
+@pytest.mark.parametrize("f16", [True, False])
+@pytest.mark.parametrize("Lq,Lk,H,Hkv", SHAPES)
+def test_a_query_that_is_not_finite(Lq, Lk, H, Hkv, f16):
+    """Its row is NaN, every other one keeps its bits; without keys it gives zeros all the same."""
+    q, k, v = att.inputs(Lq, Lk, H, Hkv, 31, Lk)
+    i, h = Lq // 2, H - 2
+    want = att.call(q, k, v, Lk, f16=f16)[:Lq].clone()
+    none = torch.full((Lq,), Lk, device="cuda")
+    none[i] = 0
+    for bad in (NAN, INF, -INF):
+        x = q.clone()
+        x[i, h, 5] = bad
+        got = att.call(x, k, v, Lk, f16=f16)[:Lq].clone()
+        assert bool(torch.isnan(got[i, h]).all())
+        got[i, h] = want[i, h]
+        assert torch.equal(got, want)
+        got = att.call(x, k, v, Lk, end=none, f16=f16)[:Lq]
+        assert bool((got[i] == 0).all()) and bool(torch.isfinite(got).all())
+
+
+@pytest.mark.parametrize("slopes", [False, True])
+@pytest.mark.parametrize("Lq,Lk,H,Hkv", SHAPES)
+def test_attended_keys_that_are_not_numbers(Lq, Lk, H, Hkv, slopes):
+    """One key of a row's many, and all of a row's keys."""
+    q, k, v = att.inputs(Lq, Lk, H, Hkv, 32, Lk)
+    sl = torch.rand(H, device="cuda") * 0.01 if slopes else None
+    g = H // Hkv
+    begin, end = torch.zeros(Lq, dtype=torch.int64, device="cuda"), torch.full((Lq,), Lk, device="cuda")
+    begin[0], end[0] = 70, 90
+    begin[1:], end[1:] = 100, Lk
+    for where in (slice(80, 81), slice(70, 90)):
+        x = k.clone()
+        x[where, Hkv - 1] = NAN
+        want = att.call(q, k, v, Lk, begin, end, slopes=sl)[:Lq]
+        got = att.call(q, x, v, Lk, begin, end, slopes=sl)[:Lq].clone()
+        assert bool(torch.isnan(got[0, H - g:]).all())
+        got[0, H - g:] = want[0, H - g:]
+        assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("Lq,Lk,H,Hkv", SHAPES)
+def test_attended_keys_of_score_minus_infinity(Lq, Lk, H, Hkv):
+    """They weigh nothing beside others; a row that has no other key has no softmax: NaN."""
+    q, k, v = att.inputs(Lq, Lk, H, Hkv, 33, Lk)
+    q[:, :, 0] = 4.0
+    x = k.clone()
+    n = Lk - Lk // 3
+    x[:n, :, 0] = -INF
+    b, e = torch.full((Lq,), n, device="cuda"), torch.full((Lq,), Lk, device="cuda")
+    ref, tol = att.formula(q, k, v, b, e, None, 0.0, None)
+    got = att.call(q, x, v, Lk, f16=False)[:Lq].double()
+    assert bool(((got - ref).abs() <= tol).all())
+    got = att.call(q, x, v, Lk, end=torch.full((Lq,), n - 3, device="cuda"), f16=False)[:Lq]
+    assert bool(torch.isnan(got).all())
