@@ -374,8 +374,9 @@ int dllm_qk_rope(const float* q, int64_t ldq, const float* k, int64_t ldk, const
  * overlap the inputs.  dh must be 128.  Lq == 0 is a no-op; Lk == 0 writes zeros.
  * What keys hold outside a query's interval (NaN, infinities, memory never written) does
  * not reach its output.  A query that holds a NaN, attends to a k with one, or has only scores of
- * -inf gives NaN (with an empty interval zeros all the same); one that attends to a v with a NaN or
- * an infinity is not finite.
+ * -inf gives NaN (with an empty interval zeros all the same).  A v with a NaN or an infinity costs the
+ * queries that attend to it that column alone: not finite, NaN or the infinity; the other columns
+ * keep their bits.
  * Precision as dllm_attention: f32 scores and softmax, weights rounded to f16 for P V.
  * workspace: device scratch owned by the caller, at least
  * dllm_attention_masked_workspace_bytes() bytes (may be 0, and at most 64 MiB); nothing in

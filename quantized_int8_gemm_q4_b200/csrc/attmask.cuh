@@ -29,8 +29,9 @@
 //   10 [6]          TMA producer of Q, K and V (4 and 8 [2 and 3] slots of 64 keys x dh)
 //   11 [7]          V's gate: in a block that some row does not see whole, it replaces what
 //                   is not finite by zeros and marks those keys (a weight of zero times NaN is
-//                   NaN, and the hidden key of one row is another's); a row that attends a
-//                   marked key becomes NaN
+//                   NaN, and the hidden key of one row is another's).  A row that attends a
+//                   marked key loses, at the end, the columns where a value of its keys from
+//                   there on is not finite, as it would where all rows see the block whole
 // Tensor memory: O of chain t at columns 256 t, two S slots of 64 columns behind it, block kb in slot
 // kb & 1; P lies over the first half of its S (f16 pairs).  Issue order per chain: S(0), S(1), then
 // P V(kb), S(kb + 2): the scores of the next block are there when a softmax ends, and the
@@ -100,6 +101,8 @@ struct MaskArgs {
     int32_t gp, tq;   // heads and queries per tile
     int32_t splits;   // parts of the key range (grid y)
     const int32_t *kv_begin, *kv_end, *q_pos;
+    const __half* v;  // as in the tensor map, for the columns of values that are not finite
+    int64_t ldv;
     float cap_in, cap_out;  // base-2 exponents: cap_out tanh(cap_in q.k)
     const float* slopes;
     void* o;
@@ -166,6 +169,9 @@ __device__ __forceinline__ void mma_f16_ts_if(uint32_t issue, uint32_t d_tmem, u
         : "memory");
 }
 
+// An f16 with all exponent bits set (infinity or NaN) carries into its sign bit, for two at a time.
+__device__ __forceinline__ uint32_t att_not_finite(uint32_t y) { return (y & 0x7fff7fffu) + 0x04000400u; }
+
 // tanh(y) = 1 - 2 / (1 + 2^(2 log2(e) y)), good to a few 2^-24 absolute.
 __device__ __forceinline__ float att_tanh(float y) {
     const float e = att_ex2(y * 2.885390081777927f);
@@ -192,6 +198,41 @@ __device__ __forceinline__ float2 att_tanh_poly(float2 y) {
     p = ffma2(p, q, k(-0.33332130312919617f));
     p = ffma2(p, q, k(0.9999997019767761f));
     return fmul2(p, y);
+}
+
+// Turns into NaN, in the warp's rows of O (tensor memory), the columns where a value of the row's keys
+// [first, end) is not finite; first >= end leaves a row as it is.  All lanes take part: 8 bytes each
+// of a key's value, row by row.  Not inlined: rare, and its registers are the hot loop's.
+__device__ __noinline__ void msk_lose_columns(uint32_t tO, int first, int end, const __half* v, int64_t ldv) {
+    const int lane = threadIdx.x & 31;
+    uint32_t lost[4] = {0, 0, 0, 0};  // bit i of word j: column 4 i + j
+#pragma unroll 1
+    for (uint32_t rows = __ballot_sync(~0u, first < end); rows; rows &= rows - 1) {
+        const int r = __ffs(rows) - 1, k1 = __shfl_sync(~0u, end, r);
+        uint32_t x = 0, y = 0;
+#pragma unroll 4
+        for (int k = __shfl_sync(~0u, first, r); k < k1; k++) {
+            const uint2 u = __ldg(reinterpret_cast<const uint2*>(v + k * ldv) + lane);
+            x |= att_not_finite(u.x);
+            y |= att_not_finite(u.y);
+        }
+        const uint32_t w[4] = {x & 0x8000u, x & 0x80000000u, y & 0x8000u, y & 0x80000000u};
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const uint32_t b = __ballot_sync(~0u, w[j] != 0);
+            if (lane == r) lost[j] = b;
+        }
+    }
+#pragma unroll 1
+    for (int c = 0; c < 8; c++) {
+        uint32_t o[16];
+        tmem_ld16(tO + 16 * c, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; e++) o[e] = lost[e & 3] >> (4 * c + (e >> 2)) & 1 ? 0x7fffffffu : o[e];
+        tmem_st16(tO + 16 * c, o);
+    }
+    tmem_wait_st();
 }
 
 // MODE bit 0: cap, bit 1: distance bias, bit 2: halves.
@@ -338,8 +379,7 @@ __global__ void __launch_bounds__(msk_threads(MODE & 4), MODE & 4 ? 1 : 2)
                     if (lane < 2) sh.flags[b][lane] = 0;
                     __syncwarp();
                     uint4* const v = reinterpret_cast<uint4*>(sV + b * MSK_KV);
-                    // an f16 with all exponent bits set carries into its sign bit
-                    auto c = [](uint32_t y) { return (y & 0x7fff7fffu) + 0x04000400u; };
+                    auto c = att_not_finite;
 #pragma unroll 1
                     for (int i0 = lane; i0 < MSK_KV / 16; i0 += 8 * 32) {
                         uint4 x[8];
@@ -442,7 +482,7 @@ __global__ void __launch_bounds__(msk_threads(MODE & 4), MODE & 4 ? 1 : 2)
         int vs = t, vp = 0;  // V slot of the present block and its parity
         const int w_lo0 = sh.lo_min[warp], w_hi1 = sh.hi_max[warp], w_lo1 = sh.lo_max[warp], w_hi0 = sh.hi_min[warp];
         const bool some = lo < hi;
-        if (!some) lo = 0, hi = a.Lk;  // a row without keys runs along; it stores zeros
+        if (!some) lo = hi = 0;  // a row without keys runs along; it stores zeros
         float slope = 0.0f;
         int qp = 0;
         if (BIAS && live) {
@@ -451,6 +491,7 @@ __global__ void __launch_bounds__(msk_threads(MODE & 4), MODE & 4 ? 1 : 2)
         }
         float m = -INFINITY, l = 0.0f;
         bool ok = true;
+        int first = INT_MAX;  // the first attended key that the gate marked
         for (int kb = kb0; kb < kb1; kb++) {
             const int sl = (kb - kb0) & 1, use = (kb - kb0) >> 1, k0 = kb * MSK_BK;
             const uint32_t tS = tO + 128 + 64 * sl;
@@ -570,8 +611,10 @@ __global__ void __launch_bounds__(msk_threads(MODE & 4), MODE & 4 ? 1 : 2)
                 if (!__all_sync(~0u, att_wait(&sh.v_ready[vs], vp))) l = NAN;
 #pragma unroll 1
                 for (int w = 0; w < 2; w++)
-                    for (uint32_t f = sh.flags[vs][w]; f; f &= f - 1)
-                        if ((uint32_t)(k0 + 32 * w + __ffs(f) - 1 - lo) < (uint32_t)(hi - lo)) l = NAN;
+                    for (uint32_t f = sh.flags[vs][w]; f; f &= f - 1) {
+                        const int key = k0 + 32 * w + __ffs(f) - 1;
+                        if ((uint32_t)(key - lo) < (uint32_t)(hi - lo)) first = min(first, key);
+                    }
             }
             tmem_wait_st();
             tc_fence_before();
@@ -586,6 +629,10 @@ __global__ void __launch_bounds__(msk_threads(MODE & 4), MODE & 4 ? 1 : 2)
             return i < 0 || __all_sync(~0u, att_wait(&sh.o_done[x][i & 1], (i >> 1) & 1));
         };
         if (ok) ok = last(t);
+        if (ok && __any_sync(~0u, first != INT_MAX)) {
+            tc_fence_after();
+            msk_lose_columns(tO, first, min(hi, kb1 * MSK_BK), a.v + hk * ATT_DH, a.ldv);
+        }
         // O = f O_t (+ fx O_other): halves join their results, in the scale of the larger maximum.
         const bool ran = kb0 < kb1, ran_x = halves && t0[t ^ 1] < t1[t ^ 1];
         float f = 1.0f, fx = 0.0f;

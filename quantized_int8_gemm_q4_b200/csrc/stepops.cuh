@@ -241,6 +241,7 @@ int dllm_attention_masked(const void* q, int64_t ldq, const void* k, int64_t ldk
     a.Lq = (int32_t)Lq, a.Lk = (int32_t)Lk, a.H = (int32_t)H, a.group = (int32_t)(H / Hkv);
     a.gp = p.gp, a.tq = p.tq, a.splits = p.splits;
     a.kv_begin = kv_begin, a.kv_end = kv_end, a.q_pos = q_pos;
+    a.v = static_cast<const __half*>(v), a.ldv = ldv;
     const double scale = 0.08838834764831844, log2e = 1.4426950408889634;  // 1 / sqrt(128)
     a.cap_in = softcap > 0.0f ? (float)(scale / softcap) : 0.0f;
     a.cap_out = (float)(softcap * log2e);

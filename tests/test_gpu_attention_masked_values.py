@@ -78,3 +78,52 @@ def test_attended_keys_of_score_minus_infinity(Lq, Lk, H, Hkv):
     assert bool(((got - ref).abs() <= tol).all())
     got = att.call(q, x, v, Lk, end=torch.full((Lq,), n - 3, device="cuda"), f16=False)[:Lq]
     assert bool(torch.isnan(got).all())
+
+
+def documents_beside(Lq, Lk):
+    """Intervals that all end inside a block of keys at 40 and begin at 0 or 20: no row sees the block whole."""
+    b = torch.where(torch.arange(Lq, device="cuda") % 2 == 0, 0, 20)
+    return b, torch.full((Lq,), Lk - 24, device="cuda")
+
+
+@pytest.mark.parametrize("bad", [NAN, INF, -INF])
+@pytest.mark.parametrize("Lq,Lk,H,Hkv", SHAPES)
+def test_an_attended_value_costs_its_own_column(Lq, Lk, H, Hkv, bad):
+    """Whether the other rows see its block whole, in part or not at all."""
+    q, k, v = att.inputs(Lq, Lk, H, Hkv, 34, Lk)
+    g = H // Hkv
+    some = torch.arange(Lq, device="cuda") % 2 == 0
+    for begin, end in ((None, None), documents_beside(Lq, Lk)):
+        want = att.call(q, k, v, Lk, begin, end)[:Lq].clone()
+        x = v.clone()
+        # keys of the first block, a middle one and the last; columns of every part of a row
+        for key, col in ((7, 3), (7, 127), (Lk // 2, 64), (Lk - 30, 40), (Lk - 2, 90)):
+            x[key, Hkv - 1, col] = bad
+        got = att.call(q, k, x, Lk, begin, end)[:Lq].clone()
+        lost = torch.zeros_like(got, dtype=torch.bool)
+        lost[:, H - g:, 64] = lost[:, H - g:, 40] = True
+        if begin is None:
+            lost[:, H - g:, 90] = True
+        sees7 = torch.ones_like(some) if begin is None else some
+        lost[sees7, H - g:, 3] = lost[sees7, H - g:, 127] = True
+        assert torch.equal(~torch.isfinite(got), lost)
+        got[lost] = want[lost]
+        assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("Lq,Lk,H,Hkv", SHAPES)
+def test_an_attended_value_of_no_weight_costs_its_column(Lq, Lk, H, Hkv):
+    """Where its score is minus infinity and that of every key around it."""
+    q, k, v = att.inputs(Lq, Lk, H, Hkv, 35, Lk)
+    q[:, :, 0] = 4.0
+    k[:Lk // 2, :, 0] = -INF
+    v[9, :, 3] = NAN
+    for begin, end in ((None, None), documents_beside(Lq, Lk)):
+        got = att.call(q, k, v, Lk, begin, end)[:Lq]
+        sees = torch.zeros(Lq, dtype=torch.bool, device="cuda") if begin is not None else None
+        if begin is not None:
+            sees = begin == 0
+            assert bool(torch.isfinite(got[~sees]).all())
+            got = got[sees]
+        assert not bool(torch.isfinite(got[:, :, 3]).any())
+        assert bool(torch.isfinite(got[:, :, :3]).all()) and bool(torch.isfinite(got[:, :, 4:]).all())
