@@ -623,7 +623,7 @@ __global__ void __launch_bounds__(msk_threads(MODE & 4), MODE & 4 ? 1 : 2)
             vs += CHAINS;
             if (vs >= v_slots) vs -= v_slots, vp ^= 1;
         }
-        // The last P V of a tile with blocks.
+        // The last P V of this chain.
         auto last = [&](int x) {
             const int i = (x ? t1[1] - t0[1] : t1[0] - t0[0]) - 1;
             return i < 0 || __all_sync(~0u, att_wait(&sh.o_done[x][i & 1], (i >> 1) & 1));
@@ -637,9 +637,14 @@ __global__ void __launch_bounds__(msk_threads(MODE & 4), MODE & 4 ? 1 : 2)
         const bool ran = kb0 < kb1, ran_x = halves && t0[t ^ 1] < t1[t ^ 1];
         float f = 1.0f, fx = 0.0f;
         if (halves) {
-            if (ok) ok = last(t ^ 1);
+            // Each of the two warps that share these rows has waited for its own chain's last P V; what hands
+            // the other's O over (and the space of Q and K, which both chains read) is this barrier.  A
+            // wait for the other's o_done here could pass early: its phases were not followed.
             sh.ml[t][row] = ran ? make_float2(m, l) : make_float2(-INFINITY, 0.0f);
+            tc_fence_after();
+            tc_fence_before();
             ok = named_barrier_and(1 + quad, 64, ok);
+            tc_fence_after();
             const float2 o = sh.ml[t ^ 1][row];
             if (!ran) m = -INFINITY, l = 0.0f;
             const float top = fmaxf(m, o.x), zero = top == -INFINITY ? 0.0f : top;
