@@ -120,18 +120,19 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-_raw_stream = _device = None
+_current_stream = None  # set in one store: another thread finds None or the whole function
 
 
 def _stream(stream):
     """The cudaStream_t to launch on.  The current one is asked for as a number: building torch's
     stream object costs more host time (3.2 us) than the launch."""
-    global _raw_stream, _device
+    global _current_stream
     if stream is None:
-        if _raw_stream is None:
+        if _current_stream is None:
             import torch
-            _raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
-        return _raw_stream(_device())
+            raw, device = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
+            _current_stream = lambda: raw(device())  # noqa: E731
+        return _current_stream()
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
