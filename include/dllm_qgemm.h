@@ -409,8 +409,12 @@ int dllm_attention_masked(const void* q, int64_t ldq, const void* k, int64_t ldk
  * token: int32 [R]; conf, entropy: f32 [R], each may be NULL.  A row with a NaN or +inf, or
  * without a finite logit, gets token -1, conf 0, entropy 0 and sets DLLM_ERR_LOGITS in the
  * device error word.  R == 0 is a no-op.
- * Weights and masses are 64-bit fixed point from an f64 exponential: the token is the same
- * whatever the grid, and the same on every run.
+ * Weights and masses are fixed point from an f64 exponential, in units of 2^-f of the largest
+ * weight with f = min(51, 62 - ceil(log2 V)) (45 up to 2^17 words): the token is the same whatever the
+ * grid, and the same on every run.  A border between two tokens is off by at most V 2^-(f + 1) of the
+ * largest weight (2^-29 at 2^17 words, 2^-15 at 2^24, 2^-7 at 2^28).  Words below half a
+ * unit are not drawn, and no min_p above 0 keeps them; without top_p and min_p, u = 0 and u = 1
+ * nevertheless give the first and the last kept word, down to a weight of 2^-1075.
  * Errors: DLLM_ERR_ARG, DLLM_ERR_ALIGN, DLLM_ERR_UNSUPPORTED, DLLM_ERR_CUDA.
  * ---------------------------------------------------------------------------- */
 int dllm_sample(const float* logits, int64_t R, int64_t V, int64_t ldl, const float* temperature, const int32_t* top_k,

@@ -10,11 +10,14 @@
 //
 // Every limit keeps a prefix of the one order, so no sort is needed: a limit is a cut
 // (value, index), found by a histogram over the values and an exact ranking of the one
-// bin it falls into.  Weights are 64-bit fixed point (at least 2^-45 of the largest at
-// 2^17 candidates) from an f64 exponential: integer sums do not depend on their order, so
-// atomics and any split over threads and CTAs give one result, and a border between two
-// tokens is off by less than 2^-36 of the mass (f32 sums put 1 row in ~400 on the wrong
-// side of one).
+// bin it falls into.  Weights are fixed point, multiples of 2^-fix of the largest with fix =
+// min(51, 62 - ceil(log2 V)) (45 at 2^17 words), from an f64 exponential: integer sums do not depend
+// on their order, so atomics and any split over threads and CTAs give one result.  A border
+// between two tokens is off by at most V 2^-(fix + 1) of the largest weight (2^-29 at 2^17 words, if a whole
+// flat tail lies just below half a unit; ~2^-38 where the roundings fall to either side; f32 sums put
+// 1 row in ~400 on the wrong side of one).  A word below half a unit weighs 0 and is not drawn.  Only
+// u at its ends, which asks for the first or the last kept word, would show that, and only without
+// top_p and min_p, which keep no such word: there every kept word weighs the same.
 //
 // One cluster of C CTAs per row.  Each CTA keeps its slice of the row in shared memory (read
 // from HBM once); every step is one pass over the slices and one cluster barrier:
@@ -92,7 +95,7 @@ struct alignas(16) SampleShared {  // the slice follows it, read in 16-byte vect
     uint32_t found_bin, found_upto, n_mine[2], n_list, best;
     u64 cut;                  // order code
     uint64_t landed;          // mbarrier: the slice is in shared memory
-    double scale, ln_min_p;   // log2(e) / T, ln(min_p)
+    double scale, ln_min_p;   // log2(e) / T (or 0: all weigh alike), ln(min_p)
 };
 
 static_assert(sizeof(SampleShared) % 16 == 0, "the slice behind it is read as float4");
@@ -468,7 +471,9 @@ __global__ void __launch_bounds__(SMP_THREADS, 2) sample_kernel(const __grid_con
         const int edge = lane == 8 && i0 > 0 ? 0 : lane == 9 && i1 < row.cached && i1 >= i0 ? i1 : -1;
         if (edge >= 0 && edge < row.cached) *reinterpret_cast<float4*>(smp_cache() + edge) = row.load4(edge);
     } else if (w == 1 && lane == 0) {
-        sm.scale = 1.4426950408889634 / Td;
+        // The first or the last kept word without a mass limit: all weigh alike, however unlikely.
+        const bool ends = (u == 0.0f || u == 1.0f) && (p >= 1.0f || k == 1) && min_p == 0.0;
+        sm.scale = ends ? 0.0 : 1.4426950408889634 / Td;
         sm.ln_min_p = min_p > 0.0 ? log(min_p) : 0.0;
     }
     static_assert(SMP_TABLE == SMP_THREADS, "one entry per thread");
@@ -508,7 +513,8 @@ __global__ void __launch_bounds__(SMP_THREADS, 2) sample_kernel(const __grid_con
         const u64(*box)[SMP_MAX_CLUSTER] = row.exchange(m1, m2, m3, 0);
         m1 = max_of(box[0], C), m2 = max_of(box[1], C), m3 = max_of(box[2], C);
     }
-    const float top = row.top = smp_value(m1), bottom = smp_value(~m2);
+    const float top = row.top = smp_value(m1);
+    const float bottom = smp_value(~m2);
     if (m3 || top == -INFINITY) {  // uniform over the cluster
         if (r == 0 && threadIdx.x == 0) {
             a.token[i_row] = -1;
@@ -527,7 +533,8 @@ __global__ void __launch_bounds__(SMP_THREADS, 2) sample_kernel(const __grid_con
     row.lowest = fmaxf(-FLT_MAX, __double2float_rd((double)top - deep * 1.000001 * Td - hair));
     row.coarse = Td < 1e-18 || ((double)top - (double)row.lowest) * row.scale > 1000.0;
     row.topd = SampleRow::widen(top);
-    row.cut_val = bottom;  // everything finite
+    // everything finite; where all weigh alike, nothing that has no weight in 64 bits either (2^-1075)
+    row.cut_val = row.scale == 0.0 ? fmaxf(bottom, __double2float_rd((double)top - 745.1332191019412 * Td)) : bottom;
     row.cut_i = INT_MAX;
 
     // plain softmax: mass and first moment of the elements below the largest, and the
@@ -594,7 +601,7 @@ __global__ void __launch_bounds__(SMP_THREADS, 2) sample_kernel(const __grid_con
         u64 target = 0, tie_mass = 0;
         if (stage < 2) {
             if (!(by_count ? k > 0 : by_p)) continue;
-            float from = fmaxf(bottom, row.cut_val), to = top;
+            float from = row.cut_val, to = top;
             if (mass) {
                 // no bins for values whose weight is 0 (with some room for either side's rounding)
                 from = fmaxf(from, row.lowest);

@@ -47,3 +47,44 @@ def test_top_k_of_many_then_top_p_of_few(R, V):
     assert dllm.dllm_get_device_status() == dllm.DLLM_OK
     for t in token:
         assert t.tolist() == want
+
+
+def tokens_of(x, T=None, k=None, p=None, mp=None, u=None):
+    """The tokens alone: a word of no more than 2^-149 has the confidence 0 in f32."""
+    R = len(x)
+    f = lambda a, d: np.full(R, d) if a is None else np.asarray(a)  # noqa: E731
+    got = smp.run(x, T, k, p, mp, u)[0].tolist()
+    T, k, p, mp, u = (f(a, d) for a, d in ((T, 1.0), (k, 0), (p, 1.0), (mp, 0.0), (u, 0.0)))
+    T, p, mp, u = (np.float32(a) for a in (T, p, mp, u))
+    want = [smp.define(x[r], float(T[r]), int(k[r]), float(p[r]), float(mp[r]), float(u[r]))[0] for r in range(R)]
+    assert got == want
+
+
+@pytest.mark.parametrize("far", [33.0, 40.0, 300.0])
+@pytest.mark.parametrize("V", [1, 2, 50, 700, 30001, 160000])
+def test_first_and_last_kept_word_however_unlikely(V, far):
+    """u at its ends takes the first and the last kept index, also where the kept words before and behind the
+    likely ones weigh less than the unit of the masses."""
+    u = np.array([0.0, 1.0, -3.0, 7.0, np.nan, 0.0, 1.0, 0.5], np.float32)
+    R = len(u)
+    for T in (0.1, 1.0, 4.0):
+        g = np.random.default_rng([V, int(far)])
+        x = (g.standard_normal((R, V)) * 0.1 * T).astype(np.float32)
+        x[:, V // 2] = np.float32(far * T)
+        x[:, :V // 9:2] = -np.inf  # ruled out: not kept
+        if V > 9:
+            x[:, V - 3:] = -np.inf
+        t = np.full(R, T)
+        tokens_of(x, T=t, u=u)
+        tokens_of(x, T=t)
+        tokens_of(x, T=t, u=u, k=np.array([V, V, 40, 40, 3, 300, 300, 2]))  # by a list of few, and by masses of many
+        tokens_of(x, T=t, u=u, p=np.full(R, 0.9))
+        tokens_of(x, T=t, u=u, mp=np.full(R, 1e-6))
+
+
+def test_words_that_weigh_nothing_in_64_bits_are_not_drawn():
+    x = np.zeros((3, 5000), np.float32)
+    x[:, 77], x[:, 3000], x[:, 4000] = 10.0, 9.5, 9.0
+    tokens_of(x, T=np.full(3, 0.01), u=np.array([0.0, 1.0, 0.5]))
+    tokens_of(x, T=np.full(3, 0.001), u=np.array([0.0, 1.0, 0.5]))
+    tokens_of(x, T=np.full(3, 0.01), u=np.array([0.0, 1.0, 0.5]), k=np.array([100, 3000, 100]))
