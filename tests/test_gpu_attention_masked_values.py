@@ -127,3 +127,21 @@ def test_an_attended_value_of_no_weight_costs_its_column(Lq, Lk, H, Hkv):
             got = got[sees]
         assert not bool(torch.isfinite(got[:, :, 3]).any())
         assert bool(torch.isfinite(got[:, :, :3]).all()) and bool(torch.isfinite(got[:, :, 4:]).all())
+
+
+@pytest.mark.parametrize("cap", [1e9, 2.0 ** 99, 2.0 ** 100])
+@pytest.mark.parametrize("Lq,Lk,H,Hkv", SHAPES[2:])
+def test_a_cap_far_above_the_scores_leaves_them_as_they_are(Lq, Lk, H, Hkv, cap):
+    """cap tanh(x / cap) = x to (x / cap)^2 relative.  The kernel's polynomial is good to 2^-22 relative there and
+    its scalings to 2^-24 each, together below 2^-20 |x|, which moves a weight by as much: 2 * 2^-20 max|x| max|v|
+    beside the tolerance of uncapped scores.  Zeros and scores under a small cap lie outside of it."""
+    q, k, v = att.inputs(Lq, Lk, H, Hkv, 36, Lk)
+    b, e = torch.full((Lq,), 3, device="cuda"), torch.full((Lq,), Lk - 5, device="cuda")
+    ref, tol = att.formula(q, k, v, b, e, None, 0.0, None)
+    x = torch.einsum("ihd,jhd->hij", q.double(), k.double().repeat_interleave(H // Hkv, 1)).abs().amax() / att.DH ** 0.5
+    tol = tol + 2 * 2.0 ** -20 * x * v.double().abs().amax()
+    got = att.call(q, k, v, Lk, b, e, cap=cap, f16=False)[:Lq].double()
+    assert bool(((got - ref).abs() <= tol).all())
+    small = att.formula(q, k, v, b, e, None, 0.5, None)[0]
+    for wrong in (torch.zeros_like(ref), small):
+        assert int(((wrong - ref).abs() > tol).sum()) > 100  # one would do
