@@ -70,12 +70,18 @@ MaskPlan mask_plan(int64_t Lq, int64_t Lk, int64_t H, int64_t Hkv, int sms) {
         int64_t n = most < blocks / 3 ? most : blocks / 3;
         while (2 * n * n > 5 * blocks) n--;
         p.splits = (int)n;
-        // One part per SM leaves a tenth of the SMs or more without work (32 heads on 148 SMs: 20): two
-        // CTAs per SM in parts of half the length leave fewer, for parts long enough that streaming
-        // the keys is all that counts (one query over 20011 keys 58.8 -> 57.0 us, over 60000
-        // 157.6 -> 147.1; 8 tiles, which leave 4 SMs idle, 49.4 -> 54.6 over 60000).
+        // One part per SM can leave SMs without work (32 tiles on 148 SMs: 20), two CTAs per SM in parts of
+        // half the length fewer.  That saves each SM 0.75 us per block, its share of HBM, and costs 0.45 us
+        // per further part, up to 1.1 us where a part has all 128 rows to write and join.  One query, one against
+        // two per SM: 32 heads, 4000 keys 19.6 and 21.3 us, 10000 34.6 and 34.9, 14500 45.8 and 44.9, 60000 163.8
+        // and 147.6; 22 heads, 20011 keys 43.9 and 44.4, 30000 60.8 and 60.1; 40 heads, 2500 keys 18.6 and
+        // 19.0, 4000 23.6 and 23.4, 10000 43.3 and 39.7; 50 heads, 2500 keys 24.1 and 21.3.  128 queries of 32
+        // heads, 14000 keys 48.0 and 50.7, 20011 68.7 and 66.9.  (8 tiles, which leave 4 SMs idle, 60000 keys
+        // 49.4 and 54.6.)
         const int64_t more = 2 * sms / p.grid;
-        if (10 * (sms - most * p.grid) >= sms && more > 2 * most && more <= blocks / 32)
+        const double saved = (double)blocks / most - 2.0 * blocks / more;
+        const double rows = (double)(Lq < p.tq ? Lq : p.tq) * p.gp;
+        if (n == most && saved > (0.6 + rows / 140) * (double)(more - most))
             p.halves = false, p.splits = (int)more;
     }
     p.ml_off = p.bytes = 0;
