@@ -21,11 +21,12 @@ bool g_att_attr_done[MAX_DEV];
 
 int current_device(int* dev) {
     if (cudaGetDevice(dev) != cudaSuccess || *dev < 0 || *dev >= MAX_DEV) return DLLM_ERR_CUDA;
-    if (g_dev_checked[*dev] == 0) {
+    if (__atomic_load_n(&g_dev_checked[*dev], __ATOMIC_ACQUIRE) == 0) {
         cudaDeviceProp p;
         if (cudaGetDeviceProperties(&p, *dev) != cudaSuccess) return DLLM_ERR_CUDA;
-        g_dev_checked[*dev] = (p.major == 10 && p.minor == 0) ? 1 : -1;
         g_num_sms[*dev] = p.multiProcessorCount;
+        // last, so that another thread's call which finds the device checked also finds its SM count
+        __atomic_store_n(&g_dev_checked[*dev], (p.major == 10 && p.minor == 0) ? 1 : -1, __ATOMIC_RELEASE);
     }
     return g_dev_checked[*dev] == 1 ? DLLM_OK : DLLM_ERR_UNSUPPORTED;
 }
