@@ -533,12 +533,13 @@ __global__ void __launch_bounds__(SMP_THREADS, 2) sample_kernel(const __grid_con
     row.lowest = fmaxf(-FLT_MAX, __double2float_rd((double)top - deep * 1.000001 * Td - hair));
     row.coarse = Td < 1e-18 || ((double)top - (double)row.lowest) * row.scale > 1000.0;
     row.topd = SampleRow::widen(top);
-    // everything finite; where all weigh alike, nothing that has no weight in 64 bits either (2^-1075)
-    row.cut_val = row.scale == 0.0 ? fmaxf(bottom, __double2float_rd((double)top - 745.1332191019412 * Td)) : bottom;
+    row.cut_val = bottom;  // everything finite
     row.cut_i = INT_MAX;
 
     // plain softmax: mass and first moment of the elements below the largest, and the
-    // number equal to it (kept apart, so that a peaked row's small entropy stays exact)
+    // number equal to it (kept apart, so that a peaked row's small entropy stays exact).  f32 within a thread
+    // (V / (256 C) terms, off by 5e-8 of conf and entropy in all at 2^17 words), f64 from there on: f64
+    // sums here would add two of the slow operations per element for figures that are rounded to f32.
     double s1 = 0.0, s2 = 0.0, s3 = 0.0;
     if (a.conf || a.entropy) {
         float e1 = 0.0f, e2 = 0.0f;
@@ -590,6 +591,8 @@ __global__ void __launch_bounds__(SMP_THREADS, 2) sample_kernel(const __grid_con
     // limit needs masses only where min_p or a mass limit follows it, or the list below ends it.
     const bool by_p = !(p >= 1.0f) && k != 1;
     const bool mass = by_p || min_p > 0.0;
+    // Where all weigh alike, nothing is kept that has no weight in 64 bits either (2^-1075).
+    if (!mass && sm.scale == 0.0) row.cut_val = fmaxf(bottom, __double2float_rd((double)top - 745.1332191019412 * Td));
     bool have = false, clear = false;  // the histogram over all candidates is there; must be cleared first
     bool cut_mass = false;
     int half = 0;       // which list comes next
