@@ -585,6 +585,8 @@ __global__ void __launch_bounds__(msk_threads(MODE & 4), MODE & 4 ? 1 : 2)
                         }
                     }
                 }
+                // P is rounded to f16, the type of V in the same MMA (the rest would double the products); l sums
+                // it unrounded.  Over the output this is ~1.1-1.8 2^-13 relative, beside 1.7 2^-13 of an f16 output.
                 const float neg = m == -INFINITY ? 0.0f : -m;
                 const float2 c2 = make_float2(C, C), n2 = make_float2(neg, neg);
                 float2 sum[2];

@@ -51,7 +51,9 @@ struct MaskPlan {
 
 // CTAs and key parts of a masked attention call.  Two CTAs share an SM once there are more tiles
 // than SMs; else each has an SM and two chains of blocks; with at most half a wave of those the
-// keys are cut into parts, up to one wave in all.
+// keys are cut into parts, up to one wave in all.  The intervals lie on the device, so the plan goes
+// by Lk: what a tile does see is dealt out over as many parts (one query of 32 heads with a window of
+// 1401 in 20011 keys 12.3 us; over a cache cut to the window fewer parts would do).
 MaskPlan mask_plan(int64_t Lq, int64_t Lk, int64_t H, int64_t Hkv, int sms) {
     MaskPlan p;
     const int group = (int)(H / Hkv);
