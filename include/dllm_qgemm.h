@@ -33,7 +33,8 @@
  *     that dllm_get_device_status() reports and clears; the kernel never traps.
  *   - dllm_quantize_act, dllm_rmsnorm_quantize, dllm_swiglu_quantize, dllm_qgemm, dllm_qkv_qgemm,
  *     dllm_attention, dllm_qk_rope, dllm_attention_masked and dllm_sample launch their kernels with
- *     programmatic dependent launch: a kernel may start while the previous kernel on the stream is finishing, and waits on the device for it to complete before
+ *     programmatic dependent launch: a kernel may start while the previous kernel on the
+ *     stream is finishing, and waits on the device for it to complete before
  *     touching any memory that kernel can write.  Before that wait the GEMM only
  *     prefetches its first weight tiles into L2, which is always safe.  Stream order
  *     is preserved as usual.

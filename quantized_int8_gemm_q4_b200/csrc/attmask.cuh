@@ -45,8 +45,8 @@
 //
 // Measured (one B200): 4096 positions under a 1000-position prefix, 32 heads: 154 us at 1965 MHz, 177 us
 // once the power cap holds the clock at 1680 MHz (820 TFLOP/s of attended pairs); six packed
-// documents over 1024 positions 16.3 us; one query over 20011 keys of 32 heads 58 us (5.7 TB/s);
-// 32 queries over 8200 keys, 28 heads on 4, 19.4 us; capped and biased, 1531 positions in three
+// documents over 1024 positions 16.7 us; one query over 20011 keys of 32 heads 58-59 us (5.6 TB/s);
+// 32 queries over 8200 keys, 28 heads on 4, 19.7 us; capped and biased, 1531 positions in three
 // documents, 39 us.
 // Measured and not kept: two tiles per CTA that share their key blocks (1200 positions of 32 heads,
 // all keys, 53 us against 42 for two CTAs; in eight documents 24.5 against 19.3; with the long

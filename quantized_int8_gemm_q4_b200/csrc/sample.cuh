@@ -33,8 +33,8 @@
 // instructions an element, a third of them f64, on pipes that take one every other cycle, and two
 // to three shared-memory atomics of 4-5 cycles each.
 //
-// Measured (one B200): 1 row of 152064 words with all limits 11.3 us; 32 rows of 126464 with top_p
-// 51 us; 256 rows with all limits 126 us (1.03 TB/s).  Steps on the way: f64 exponentials of the math
+// Measured (one B200): 1 row of 152064 words with all limits 11.3-12.3 us; 32 rows of 126464 with
+// top_p 51 us; 256 rows with all limits 124-127 us (1.03 TB/s).  Steps on the way: f64 exponentials of the math
 // library, a histogram per limit, 1024 threads 60 / 139 / 934 us; one histogram for both limits,
 // two CTAs per SM 39 / 79 / 385; weights by table 22 / 52 / 221; bulk copies and the list of few
 // candidates 15.5 / 62 / 177; 256 threads at 128 registers 14.4 / 60 / 158; coarse sums by vector
