@@ -10,19 +10,15 @@ def test_the_first_call_may_come_from_two_threads(monkeypatch):
     import torch
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 40 + device, raising=False)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 2)
-    own = [n for n in ("_current_stream", "_raw_stream", "_device") if n in vars(dllm)]  # what the set-up stores
-    assert own
-    for n in own:
-        monkeypatch.setattr(dllm, n, None)
+    monkeypatch.setattr(dllm, "_current_stream", None)
     seen = []
 
     def step(frame, event, arg):
         frame.f_trace_opcodes = True
         if event == "opcode" and frame.f_code is dllm._stream.__code__:
-            before = {n: getattr(dllm, n) for n in own}
+            before = dllm._current_stream
             seen.append(dllm._stream(None))  # the other thread's call, here
-            for n, x in before.items():
-                setattr(dllm, n, x)
+            dllm._current_stream = before
         return step
 
     old = sys.gettrace()

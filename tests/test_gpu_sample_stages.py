@@ -88,3 +88,20 @@ def test_words_that_weigh_nothing_in_64_bits_are_not_drawn():
     tokens_of(x, T=np.full(3, 0.01), u=np.array([0.0, 1.0, 0.5]))
     tokens_of(x, T=np.full(3, 0.001), u=np.array([0.0, 1.0, 0.5]))
     tokens_of(x, T=np.full(3, 0.01), u=np.array([0.0, 1.0, 0.5]), k=np.array([100, 3000, 100]))
+
+
+@pytest.mark.parametrize("R,V", [(6, 900), (6, 40000), (2, 152064)])
+def test_words_masked_with_the_lowest_float(R, V):
+    """They are finite, weigh nothing and are not drawn, at the first index, the last and where only they follow."""
+    low = float(np.finfo(np.float32).min)
+    x, g = smp.logits_of(R, V, 37)
+    x[:, :7], x[:, V // 3:V // 2], x[:, -9:] = low, low, low
+    x[1] = np.where(x[1] == low, -np.inf, x[1])
+    x[1, 3] = low
+    for u in (np.zeros(R), np.ones(R), g.uniform(0, 1, R)):
+        smp.check(x, u=u)
+        smp.check(x, k=np.full(R, V - 5), u=u)
+        smp.check(x, k=g.integers(1, 400, R), u=u)
+        smp.check(x, T=g.uniform(0.3, 2.0, R), p=g.uniform(0.3, 1.0, R), mp=np.full(R, 0.001), u=u)
+    x[0] = low  # a row of nothing else: all alike
+    smp.check(x[:1], u=np.array([0.3]))
